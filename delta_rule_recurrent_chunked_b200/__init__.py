@@ -10,6 +10,10 @@ is no CPU fallback, and a missing library is an error.
     out, S_final, u = scan_ex(q, k, v, beta, gate, S0=None, mode="gdn2", erase=b, write=w)
     out, S_final, A_final = vla_scan(q, k, v, u, S0=None, A0=None, lambda0=1.0)
     out = decode_step(q, k, v, beta, gate, S, mode="gdn")     # S updated in place
+
+Around a scan: short_conv / short_conv_step (the causal convolution that makes its inputs),
+ssm_scan / ssm_step (the selective state space scan), gated_norm (its output with the gate) and
+block_norm (residual and norms between blocks).
 """
 from __future__ import annotations
 
@@ -32,8 +36,27 @@ VLA_NOALLOC_MAX_FLOATS = 16777216
 MODES = {"linear": DR_LINEAR, "deltanet": DR_DELTANET, "gdn": DR_GDN, "kda": DR_KDA,
          "gdn2": DR_GDN2}
 
+CONV_SILU = 0x1000
+SSM_DT_SOFTPLUS, SSM_DT_BF16 = 0x1000, 0x2000
+NORM_SIGMOID, NORM_GATE_FIRST, NORM_SHARED_WEIGHT = 0x1000, 0x2000, 0x4000
+NORM_RESIDUAL_F32 = 0x1000
+
+
+class DrView(ctypes.Structure):
+    """dr_view: a pointer and the element strides of batch, head and token."""
+    _fields_ = [("data", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sh", ctypes.c_longlong),
+                ("st", ctypes.c_longlong)]
+
+
+class ConvSplit(ctypes.Structure):
+    """conv_split: where heads x dim channels of a short convolution go."""
+    _fields_ = [("out", DrView), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("normalise", ctypes.c_int)]
+
+
 # Every function the C ABI exports, with its ctypes signature.
 _VP, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+_PV, _PS, _LL = ctypes.POINTER(DrView), ctypes.POINTER(ConvSplit), ctypes.c_longlong
 SIGNATURES = {
     "dr_scan_fwd": ([_VP] * 8 + [_I] * 6 + [_VP], _I),
     "dr_scan_fwd_ex": ([_VP] * 11 + [_I] * 6 + [_VP], _I),
@@ -43,6 +66,12 @@ SIGNATURES = {
     "vla_scan_fwd_ex": ([_VP] * 7 + [_F] + [_VP] * 4 + [_I] * 5 + [_VP], _I),
     "vla_scan_fwd_noalloc": ([_VP] * 7 + [_F] + [_VP] * 4 + [_I] * 5 + [_VP], _I),
     "loglinear_scan_fwd": ([_VP] * 5 + [_I] * 7 + [_VP], _I),
+    "short_conv_fwd": ([_PV] + [_VP] * 4 + [_PS, _I, _VP, _F] + [_I] * 5 + [_VP], _I),
+    "short_conv_step": ([_PV] + [_VP] * 3 + [_PS, _I, _F] + [_I] * 4 + [_VP], _I),
+    "ssm_scan_fwd": ([_PV, _PV, _VP, _PV, _PV] + [_VP] * 4 + [_PV, _VP] + [_I] * 7 + [_VP], _I),
+    "ssm_step": ([_PV, _PV, _VP, _PV, _PV] + [_VP] * 3 + [_PV] + [_I] * 6 + [_VP], _I),
+    "gated_norm_fwd": ([_PV, _PV, _VP, _PV, _F] + [_I] * 6 + [_VP], _I),
+    "block_norm_fwd": ([_VP, _LL] + [_VP] * 4 + [_F, _VP, _VP, _F, _LL, _I, _I, _VP], _I),
     "dr_status_string": ([_I], ctypes.c_char_p),
     "dr_poll_error": ([_VP], _I),
     "dr_debug_timeout_probe": ([_I, _VP], _I),
@@ -456,3 +485,274 @@ def chunked_applies(mode, dtype_is_bf16: bool, dk: int, dv: int) -> bool:
     variant = MODES[mode] if isinstance(mode, str) else int(mode)
     return (dtype_is_bf16 and dk == 128 and dv in (32, 64, 128)
             and variant in (DR_DELTANET, DR_GDN, DR_KDA, DR_GDN2))
+
+
+# ---- around a scan: short convolution, selective state space scan, norms
+
+
+def _check_rows(t, name, shape, dtype, device):
+    """A tensor of `shape` with contiguous last dimension, in any layout."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+
+
+def _run(name, device, *args):
+    """Call an entry point with the device's current stream, with that device current."""
+    import torch
+
+    fn = getattr(lib(), name)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream_handle(device))
+    else:
+        rc = fn(*args, _stream_handle(device))
+    if rc != DR_OK:
+        raise DrScanError(rc, name)
+
+
+def _compute_dtype(t, name):
+    import torch
+
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bf16 or fp32")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return DR_IN_BF16 if t.dtype == torch.bfloat16 else 0
+
+
+def _check_lengths(lengths, B, device):
+    import torch
+
+    if lengths is not None:
+        _check(lengths, "lengths", (B,), torch.int32, device)
+
+
+def _conv_splits(splits, C, K):
+    splits = [(int(s[0]), int(s[1]), bool(s[2]) if len(s) > 2 else False) for s in splits]
+    if sum(h * d for h, d, _ in splits) != C:
+        raise ValueError(f"splits must cover the {C} channels")
+    return splits
+
+
+def short_conv(x, weight, bias=None, splits=None, state0=None, lengths=None, silu=True, eps=1e-6,
+               outs=None, want_state=True):
+    """Causal convolution over tokens, split into heads, through short_conv_fwd.
+    x: [B,T,C] bf16 or fp32, contiguous channels; weight: [C,K] fp32; bias: [C] fp32 or None;
+    splits: (heads, dim, normalise) for neighbouring channels, together all C (default: heads
+    of 128); state0: [B,K-1,C] like x or None; lengths: [B] int32 or None; outs: a
+    [B,heads,T,dim] tensor for each split, in any layout with contiguous channels. Returns
+    (list of outputs, state_final [B,K-1,C] or None)."""
+    import torch
+
+    mode = _compute_dtype(x, "x")
+    B, T, C = x.shape
+    K = weight.shape[-1]
+    dev = x.device
+    _check_rows(x, "x", (B, T, C), x.dtype, dev)
+    _check(weight, "weight", (C, K), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (C,), torch.float32, dev)
+    if state0 is not None:
+        _check(state0, "state0", (B, K - 1, C), x.dtype, dev)
+    _check_lengths(lengths, B, dev)
+    splits = _conv_splits(splits or [(C // 128, 128)], C, K)
+    if outs is None:
+        outs = [torch.empty((B, h, T, d), dtype=x.dtype, device=dev) for h, d, _ in splits]
+    if len(outs) != len(splits):
+        raise ValueError(f"outs must hold {len(splits)} tensors")
+    arr = (ConvSplit * len(splits))()
+    for i, ((h, d, n), o) in enumerate(zip(splits, outs)):
+        _check_rows(o, f"outs[{i}]", (B, h, T, d), x.dtype, dev)
+        arr[i] = ConvSplit(DrView(o.data_ptr(), *o.stride()[:3]), h, d, n)
+    state = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if want_state else None
+    _run("short_conv_fwd", dev, DrView(x.data_ptr(), x.stride(0), 0, x.stride(1)), _ptr(weight),
+         _ptr(bias), _ptr(state0), _ptr(lengths), arr, len(splits), _ptr(state), float(eps), B, T,
+         C, K, mode | (CONV_SILU if silu else 0))
+    return list(outs), state
+
+
+def short_conv_step(x, weight, bias=None, splits=None, state=None, silu=True, eps=1e-6, outs=None):
+    """One token of short_conv on a resident state, through short_conv_step. x: [B,C]; state:
+    [B,K-1,C] like x, shifted in place. Returns the outputs, [B,heads,dim] for each split."""
+    import torch
+
+    mode = _compute_dtype(x, "x")
+    B, C = x.shape
+    K = weight.shape[-1]
+    dev = x.device
+    _check_rows(x, "x", (B, C), x.dtype, dev)
+    _check(weight, "weight", (C, K), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (C,), torch.float32, dev)
+    if state is None:
+        raise ValueError("short_conv_step needs the state (updated in place)")
+    _check(state, "state", (B, K - 1, C), x.dtype, dev)
+    splits = _conv_splits(splits or [(C // 128, 128)], C, K)
+    if outs is None:
+        outs = [torch.empty((B, h, d), dtype=x.dtype, device=dev) for h, d, _ in splits]
+    if len(outs) != len(splits):
+        raise ValueError(f"outs must hold {len(splits)} tensors")
+    arr = (ConvSplit * len(splits))()
+    for i, ((h, d, n), o) in enumerate(zip(splits, outs)):
+        _check_rows(o, f"outs[{i}]", (B, h, d), x.dtype, dev)
+        arr[i] = ConvSplit(DrView(o.data_ptr(), o.stride(0), o.stride(1), 0), h, d, n)
+    _run("short_conv_step", dev, DrView(x.data_ptr(), x.stride(0), 0, 0), _ptr(weight),
+         _ptr(bias), _ptr(state), arr, len(splits), float(eps), B, C, K,
+         mode | (CONV_SILU if silu else 0))
+    return list(outs)
+
+
+def _ssm_common(x, dt, A, B, C, D, dt_bias, dt_softplus, rows, force_sequential=False):
+    """Checks that ssm_scan and ssm_step share; rows: the dimensions between batch and channels
+    of x ((H, T) or (H,)). Returns (mode, N, G)."""
+    import torch
+
+    mode = _compute_dtype(x, "x")
+    dev, H = x.device, rows[0]
+    G, N = B.shape[1], B.shape[-1]
+    _check_rows(x, "x", x.shape, x.dtype, dev)
+    _check_rows(B, "B", (x.shape[0], G, *rows[1:], N), x.dtype, dev)
+    _check_rows(C, "C", (x.shape[0], G, *rows[1:], N), x.dtype, dev)
+    if dt.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dt must be bf16 or fp32")
+    if dt.shape != x.shape[:-1] or dt.device != dev:
+        raise ValueError(f"dt must have shape {tuple(x.shape[:-1])} on {dev}, got "
+                         f"{tuple(dt.shape)} on {dt.device}")
+    _check(A, "A", (H,), torch.float32, dev)
+    if D is not None:
+        _check(D, "D", (H,), torch.float32, dev)
+    if dt_bias is not None:
+        _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
+    if dt.dtype == torch.bfloat16:
+        mode |= SSM_DT_BF16
+    if dt_softplus:
+        mode |= SSM_DT_SOFTPLUS
+    if force_sequential:
+        mode |= DR_FORCE_SEQUENTIAL
+    return mode, N, G
+
+
+def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, S0=None, lengths=None,
+             want_state=True, out=None, S_final=None, force_sequential=False):
+    """Selective state space scan, through ssm_scan_fwd: S = exp(delta A) S + delta x B^T,
+    y = S C + D x, delta = softplus(dt + dt_bias). x: [B,H,T,P]; B, C: [B,G,T,N] (bf16 or fp32
+    like x); all in any layout with contiguous channels; dt: [B,H,T] bf16 or fp32, any strides;
+    A, D, dt_bias: [H] fp32; S0: [B,H,P,N] fp32 or None; lengths: [B] int32 or None (rows of out
+    behind a sequence are left as they were). Returns (out like x, S_final fp32 or None)."""
+    import torch
+
+    nb, H, T, P = x.shape
+    dev = x.device
+    mode, N, G = _ssm_common(x, dt, A, B, C, D, dt_bias, dt_softplus, (H, T), force_sequential)
+    if S0 is not None:
+        _check(S0, "S0", (nb, H, P, N), torch.float32, dev)
+    _check_lengths(lengths, nb, dev)
+    if out is None:
+        out = torch.empty((nb, H, T, P), dtype=x.dtype, device=dev)
+    _check_rows(out, "out", (nb, H, T, P), x.dtype, dev)
+    if want_state and S_final is None:
+        S_final = torch.empty((nb, H, P, N), dtype=torch.float32, device=dev)
+    if S_final is not None:
+        _check(S_final, "S_final", (nb, H, P, N), torch.float32, dev)
+    _run("ssm_scan_fwd", dev, DrView(x.data_ptr(), *x.stride()[:3]),
+         DrView(dt.data_ptr(), *dt.stride()), _ptr(A), DrView(B.data_ptr(), *B.stride()[:3]),
+         DrView(C.data_ptr(), *C.stride()[:3]), _ptr(D), _ptr(dt_bias), _ptr(S0), _ptr(lengths),
+         DrView(out.data_ptr(), *out.stride()[:3]), _ptr(S_final), nb, H, G, T, P, N, mode)
+    return out, S_final
+
+
+def ssm_step(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, S=None, out=None):
+    """One token of ssm_scan on a resident state, through ssm_step. x: [B,H,P]; dt: [B,H];
+    B, C: [B,G,N]; S: [B,H,P,N] fp32, updated in place. Returns out [B,H,P] like x."""
+    import torch
+
+    nb, H, P = x.shape
+    dev = x.device
+    mode, N, G = _ssm_common(x, dt, A, B, C, D, dt_bias, dt_softplus, (H,))
+    if S is None:
+        raise ValueError("ssm_step needs the state S (updated in place)")
+    _check(S, "S", (nb, H, P, N), torch.float32, dev)
+    if out is None:
+        out = torch.empty((nb, H, P), dtype=x.dtype, device=dev)
+    _check_rows(out, "out", (nb, H, P), x.dtype, dev)
+    _run("ssm_step", dev, DrView(x.data_ptr(), x.stride(0), x.stride(1), 0),
+         DrView(dt.data_ptr(), dt.stride(0), dt.stride(1), 0), _ptr(A),
+         DrView(B.data_ptr(), B.stride(0), B.stride(1), 0),
+         DrView(C.data_ptr(), C.stride(0), C.stride(1), 0), _ptr(D), _ptr(dt_bias), _ptr(S),
+         DrView(out.data_ptr(), out.stride(0), out.stride(1), 0), nb, H, G, P, N, mode)
+    return out
+
+
+def gated_norm(y, gate, weight, norm_heads=1, act="silu", gate_first=False, eps=1e-6, out=None):
+    """RMS norm of a scan's output with its gate, through gated_norm_fwd. y: [B,H,T,d] in any
+    layout with contiguous channels; gate: [B,T,H*d] like y, or None; weight: [H*d] fp32, or [d]
+    for every head; norm_heads: neighbouring heads that are normalised together; act: "silu" or
+    "sigmoid"; gate_first: the gate before the norm. Returns [B,T,H*d]."""
+    import torch
+
+    mode = _compute_dtype(y, "y")
+    B, H, T, d = y.shape
+    dev = y.device
+    _check_rows(y, "y", (B, H, T, d), y.dtype, dev)
+    if gate is not None:
+        _check_rows(gate, "gate", (B, T, H * d), y.dtype, dev)
+    shared = weight.shape == (d,) and H != 1
+    _check(weight, "weight", (d,) if shared else (H * d,), torch.float32, dev)
+    if act not in ("silu", "sigmoid"):
+        raise ValueError(f'act must be "silu" or "sigmoid", got {act!r}')
+    if out is None:
+        out = torch.empty((B, T, H * d), dtype=y.dtype, device=dev)
+    _check_rows(out, "out", (B, T, H * d), y.dtype, dev)
+    mode |= ((NORM_SIGMOID if act == "sigmoid" else 0) | (NORM_GATE_FIRST if gate_first else 0)
+             | (NORM_SHARED_WEIGHT if shared else 0))
+    g = None if gate is None else DrView(gate.data_ptr(), gate.stride(0), 0, gate.stride(1))
+    _run("gated_norm_fwd", dev, DrView(y.data_ptr(), *y.stride()[:3]), g, _ptr(weight),
+         DrView(out.data_ptr(), out.stride(0), 0, out.stride(1)), float(eps), B, H, T, d,
+         int(norm_heads), mode)
+    return out
+
+
+def block_norm(x, weight, residual=None, scale=1.0, post_weight=None, residual_dtype=None,
+               eps=1e-6, out=None, residual_out=None):
+    """Residual and norms between two blocks, through block_norm_fwd: z = x (or its RMS norm
+    times post_weight), r = residual + scale z, out = RMS norm of r times weight. x: [...,D] bf16
+    or fp32, rows at one pitch; residual: the same shape, contiguous, like x or fp32, or None;
+    weight, post_weight: [D] fp32; scale: a number or [D] fp32; residual_dtype: of r where there
+    is no residual (default: x's). Returns (out like x, r)."""
+    import torch
+
+    mode = _compute_dtype(x, "x")
+    D, dev = x.shape[-1], x.device
+    rows = x.numel() // D if D else 0
+    x2 = x if x.dim() == 2 else x.view(rows, D)
+    _check_rows(x2, "x", (rows, D), x.dtype, dev)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    if post_weight is not None:
+        _check(post_weight, "post_weight", (D,), torch.float32, dev)
+    scale_v = scale if torch.is_tensor(scale) else None
+    if scale_v is not None:
+        _check(scale_v, "scale", (D,), torch.float32, dev)
+    rt = residual.dtype if residual is not None else residual_dtype or x.dtype
+    if rt not in (x.dtype, torch.float32):
+        raise ValueError(f"residual must be {x.dtype} or fp32, got {rt}")
+    if residual is not None:
+        if residual_dtype not in (None, rt):
+            raise ValueError(f"residual is {rt}, not {residual_dtype}")
+        _check(residual, "residual", x.shape, rt, dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    _check(out, "out", x.shape, x.dtype, dev)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=rt, device=dev)
+    _check(residual_out, "residual_out", x.shape, rt, dev)
+    _run("block_norm_fwd", dev, _ptr(x2), x2.stride(0), _ptr(residual), _ptr(weight),
+         _ptr(post_weight), _ptr(scale_v), 1.0 if scale_v is not None else float(scale),
+         _ptr(out), _ptr(residual_out), float(eps), rows, D,
+         mode | (NORM_RESIDUAL_F32 if mode and rt == torch.float32 else 0))
+    return out, residual_out

@@ -1,0 +1,54 @@
+// What the kernels around the scans share (short convolution, selective scan, norms): 16-byte
+// vectors of bf16 or fp32 values as fp32 registers, and the activations.
+#pragma once
+
+#include "common.cuh"
+
+namespace drscan {
+
+// VEC values of a tensor's type in one 16-byte access, unpacked to fp32.
+template <typename T>
+struct Vec16;
+
+template <>
+struct Vec16<float> {
+    static constexpr int N = 4;
+    __device__ __forceinline__ static void unpack(const uint4& r, float* x) {
+        x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y);
+        x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
+    }
+    __device__ __forceinline__ static uint4 pack(const float* x) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                          __float_as_uint(x[3]));
+    }
+};
+
+template <>
+struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    // a bf16 value is the upper half of its fp32 value
+    __device__ __forceinline__ static void unpack(const uint4& r, float* x) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ static uint4 pack(const float* x) {
+        return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                          pack_bf16(x[6], x[7]));
+    }
+};
+
+// 1 / (1 + e^-x): e^-x overflows to infinity for x < -88, where the quotient is 0 (so x times
+// it is -0, the limit). __fdividef would return 0 for denominators above 2^126 only, which is
+// the same limit.
+__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// log(1 + e^x) without overflow: max(x, 0) + log1p(e^-|x|).
+__device__ __forceinline__ float softplus_f32(float x) {
+    return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
+}
+
+}  // namespace drscan

@@ -1,0 +1,206 @@
+// Short causal convolution over tokens, one filter of K = 2..4 taps per channel, with SiLU, an
+// optional L2 norm per head and the split of the channels into heads:
+//
+//     c_t[ch] = bias[ch] + sum_j w[ch][j] x_{t-K+1+j}[ch],    y = c sigmoid(c)
+//     y_head <- y_head / sqrt(sum y_head^2 + eps)             (heads of a normalised split)
+//
+// x_{-1}, x_{-2}, .. come from state0, the K - 1 inputs before the sequence (zeros without it).
+//
+// Bound: HBM. Every input is read once and every output written once, at about K + 6 flops per
+// 2 bytes. A warp owns 32 vectors of 16 bytes (256 bf16 channels) of one split and walks a tile
+// of tokens; the last K - 1 rows stay in registers as the window, so a tile re-reads K - 1 rows
+// of its neighbour only. Eight rows are loaded before the first is used. A head is 4 to 32
+// neighbouring lanes, so its norm is a few shuffles and the head-major (or token-major) rows
+// leave in 16-byte stores.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace drscan {
+
+constexpr int CONV_MAX_SPLITS = 4;
+constexpr int CONV_WARPS = 4;
+constexpr int CONV_ROWS = 8;  // rows in flight per thread
+
+struct ConvSplit {
+    void* out;
+    long sb, sh, st;
+    int dim, normalise;
+    int vec0;   // first 16-byte vector of the split within a row
+    int nvec;   // vectors of the split
+    int warp0;  // first warp column of the split
+};
+
+struct ConvArgs {
+    const void* x;
+    long xsb, xst;
+    const float *weight, *bias;
+    const void* state0;
+    void* state_final;
+    const int* lengths;
+    ConvSplit split[CONV_MAX_SPLITS];
+    int nsplit, ncols;  // ncols: warp columns of all splits
+    float eps;
+    int B, T, C, tile;
+};
+
+// The split that warp column `col` belongs to.
+__device__ __forceinline__ int split_of(const ConvArgs& a, int col) {
+    int si = 0;
+    while (si + 1 < a.nsplit && col >= a.split[si + 1].warp0) ++si;
+    return si;
+}
+
+// Sum over `lanes` (a power of two) neighbouring lanes.
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+    for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// The taps of one thread's channels.
+template <int VEC, int K>
+struct ConvTaps {
+    float w[K][VEC], b[VEC];
+    __device__ __forceinline__ void load(const float* weight, const float* bias, int ch0) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            b[v] = bias ? bias[ch0 + v] : 0.f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][v] = weight[(ch0 + v) * K + j];
+        }
+    }
+};
+
+// One row: window (oldest first) and the new row x -> the activated, normalised outputs.
+template <int VEC, int K, bool SILU>
+__device__ __forceinline__ void conv_row(const ConvTaps<VEC, K>& f, float (&win)[K - 1][VEC],
+                                         const float* x, bool normalise, int lanes, float eps,
+                                         float* y) {
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+        float c = fmaf(f.w[K - 1][v], x[v], f.b[v]);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) c = fmaf(f.w[j][v], win[j][v], c);
+        y[v] = SILU ? c * sigmoid_f32(c) : c;
+        ss = fmaf(y[v], y[v], ss);
+    }
+#pragma unroll
+    for (int j = 0; j < K - 2; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) win[j][v] = win[j + 1][v];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) win[K - 2][v] = x[v];
+    if (normalise) {
+        const float r = rsqrtf(group_sum(ss, lanes) + eps);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) y[v] *= r;
+    }
+}
+
+// grid: (warp columns * B, token tiles / CONV_WARPS); block: CONV_WARPS warps, one token tile
+// each.
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_kernel(
+    const __grid_constant__ ConvArgs a) {
+    constexpr int VEC = Vec16<T>::N;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long b = blockIdx.x / a.ncols;
+    const int col = (int)(blockIdx.x % a.ncols);
+    const ConvSplit& sp = a.split[split_of(a, col)];
+    const int v_in = (col - sp.warp0) * 32 + lane;  // vector within the split
+    // lanes behind the split's last vector repeat it and store nothing: heads are whole powers
+    // of two of lanes, so no head mixes live and idle lanes
+    const bool live = v_in < sp.nvec;
+    const int v = live ? v_in : sp.nvec - 1;
+    const int ch0 = (sp.vec0 + v) * VEC;
+    const int len = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
+    const int tile = (int)blockIdx.y * CONV_WARPS + warp;
+    const long t_begin = (long)tile * a.tile;
+    const int t0 = (int)min(t_begin, (long)a.T);
+    const int t1 = (int)min(t_begin + a.tile, (long)len);
+
+    const T* xrow = static_cast<const T*>(a.x) + b * a.xsb + ch0;
+    const T* prev = a.state0 ? static_cast<const T*>(a.state0) + b * (long)(K - 1) * a.C + ch0
+                             : nullptr;
+    // row i of the K - 1 earlier inputs followed by the sequence
+    auto row = [&](long i) -> uint4 {
+        if (i >= K - 1) return *reinterpret_cast<const uint4*>(xrow + (i - (K - 1)) * a.xst);
+        if (prev) return *reinterpret_cast<const uint4*>(prev + i * a.C);
+        return make_uint4(0, 0, 0, 0);
+    };
+
+    if (tile == 0 && a.state_final && live) {
+        T* dst = static_cast<T*>(a.state_final) + b * (long)(K - 1) * a.C + ch0;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+            *reinterpret_cast<uint4*>(dst + (long)j * a.C) = row((long)len + j);
+    }
+    if (t0 >= t1) return;  // the whole warp
+
+    ConvTaps<VEC, K> f;
+    f.load(a.weight, a.bias, ch0);
+    float win[K - 1][VEC];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) Vec16<T>::unpack(row((long)t0 + j), win[j]);
+
+    const int lanes = sp.dim / VEC;
+    const int head = v / lanes, within = v % lanes;
+    T* dst = static_cast<T*>(sp.out) + b * sp.sb + head * sp.sh + within * VEC;
+    for (int t = t0; t < t1; t += CONV_ROWS) {
+        uint4 raw[CONV_ROWS];
+#pragma unroll
+        for (int i = 0; i < CONV_ROWS; ++i)
+            raw[i] = *reinterpret_cast<const uint4*>(xrow + (long)min(t + i, t1 - 1) * a.xst);
+#pragma unroll
+        for (int i = 0; i < CONV_ROWS; ++i) {
+            float x[VEC], y[VEC];
+            Vec16<T>::unpack(raw[i], x);
+            conv_row<VEC, K, SILU>(f, win, x, sp.normalise, lanes, a.eps, y);
+            if (live && t + i < t1)
+                *reinterpret_cast<uint4*>(dst + (long)(t + i) * sp.st) = Vec16<T>::pack(y);
+        }
+    }
+}
+
+// One token per sequence on a resident state (the last K - 1 inputs, shifted in place). A warp
+// per 32 vectors and sequence. grid: warp columns * ceil(B / CONV_WARPS).
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_step_kernel(
+    const __grid_constant__ ConvArgs a) {
+    constexpr int VEC = Vec16<T>::N;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long b = (long)(blockIdx.x / a.ncols) * CONV_WARPS + warp;
+    if (b >= a.B) return;  // the whole warp
+    const int col = (int)(blockIdx.x % a.ncols);
+    const ConvSplit& sp = a.split[split_of(a, col)];
+    const int v_in = (col - sp.warp0) * 32 + lane;
+    const bool live = v_in < sp.nvec;
+    const int v = live ? v_in : sp.nvec - 1;
+    const int ch0 = (sp.vec0 + v) * VEC;
+    T* state = static_cast<T*>(a.state_final) + b * (long)(K - 1) * a.C + ch0;
+    uint4 old[K - 1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        old[j] = *reinterpret_cast<const uint4*>(state + (long)j * a.C);
+    const uint4 now = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + b * a.xsb + ch0);
+    ConvTaps<VEC, K> f;
+    f.load(a.weight, a.bias, ch0);
+    float win[K - 1][VEC], x[VEC], y[VEC];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) Vec16<T>::unpack(old[j], win[j]);
+    Vec16<T>::unpack(now, x);
+    const int lanes = sp.dim / VEC;
+    conv_row<VEC, K, SILU>(f, win, x, sp.normalise, lanes, a.eps, y);
+    __syncwarp();  // idle lanes have read the last vector's state before its owner shifts it
+    if (live) {
+#pragma unroll
+        for (int j = 0; j < K - 2; ++j)
+            *reinterpret_cast<uint4*>(state + (long)j * a.C) = old[j + 1];
+        *reinterpret_cast<uint4*>(state + (long)(K - 2) * a.C) = now;
+        T* dst = static_cast<T*>(sp.out) + b * sp.sb + (v / lanes) * sp.sh + (v % lanes) * VEC;
+        *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(y);
+    }
+}
+
+}  // namespace drscan

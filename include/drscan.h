@@ -2,7 +2,7 @@
  * drscan: forward recurrent-memory scan of delta-rule linear attention on B200 (sm_100a).
  *
  * C ABI. Every tensor argument is a DEVICE pointer owned by the caller, row-major and
- * contiguous; the library never allocates, frees or keeps a pointer past the call.
+ * contiguous (or a dr_view, which carries strides); the library never allocates, frees or keeps a pointer past the call.
  * Calls are asynchronous on `stream`: the return value covers argument validation and
  * the kernel launch only. Conditions detected on the device (a bounded wait that ran
  * out) are latched in a per-device status word and read by dr_poll_error().
@@ -324,6 +324,156 @@ int vla_scan_fwd_noalloc(const float* q, const float* k, const float* v, const f
 int loglinear_scan_fwd(const void* q, const void* k, const void* v, const float* lambda,
                        void* out, int B, int H, int T, int dk, int dv, int L, int mode,
                        cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Around a scan: short convolution, selective state space scan, norms
+ * ---------------------------------------------------------------------------------------
+ */
+
+/* A tensor of B x H x T rows of contiguous channels, with element strides of batch, head and
+ * token, so that a projection's columns, [B,H,T,d] and [B,T,H,d] are all read and written in
+ * place. The data is 16-byte aligned; the strides are >= 0 and whole multiples of 16 bytes (0
+ * repeats a row; not in an output, whose strides are at least a row). A stride whose dimension
+ * has size one, or that the argument's description leaves out, is not used. */
+typedef struct dr_view {
+    void* data;
+    long long sb, sh, st;
+} dr_view;
+
+/* One split of a short convolution's channels: heads x dim neighbouring channels, written as
+ * [B,heads,T,dim]; normalise != 0 divides every head's row by its L2 norm. */
+typedef struct conv_split {
+    dr_view out;
+    int heads, dim, normalise;
+} conv_split;
+
+/* mode flags of the functions below (with DR_IN_BF16 where stated) */
+#define CONV_SILU 0x1000        /* y = c sigmoid(c) after the convolution */
+#define SSM_DT_SOFTPLUS 0x1000  /* delta = softplus(dt + dt_bias), else dt + dt_bias */
+#define SSM_DT_BF16 0x2000      /* dt is bf16 (else fp32) */
+#define NORM_SIGMOID 0x1000     /* the gate's activation is sigmoid (else silu) */
+#define NORM_GATE_FIRST 0x2000  /* the gate before the norm (else after it) */
+#define NORM_SHARED_WEIGHT 0x4000 /* weight [d], the same for every head (else [H d]) */
+#define NORM_RESIDUAL_F32 0x1000  /* residual and residual_out are fp32 beside bf16 x and out */
+
+/*
+ * short_conv_fwd -- causal convolution over tokens, K taps per channel, split into heads: what
+ * q, k, v of a delta-rule layer, or x, B, C of a state space layer, pass before their scan.
+ *
+ *     c_t = bias + sum_{j<K} weight[:,j] x_{t-K+1+j}       (rows before the first: state0)
+ *     y_t = c_t sigmoid(c_t) with CONV_SILU, else c_t
+ *     head row of a normalised split: y / sqrt(sum y^2 + eps)
+ *
+ *   x            [B,T,C] view (sb, st; st >= C), bf16 if (mode & DR_IN_BF16) else fp32
+ *   weight       [C,K] fp32, tap K - 1 on the current token; bias [C] fp32 or NULL
+ *   state0       [B,K-1,C] like x: the K - 1 inputs before the sequence, oldest first; or NULL
+ *                for zeros
+ *   lengths      [B] int32 on the device, or NULL: tokens of each sequence (clamped to 0..T).
+ *                Outputs of later rows are left as they were; rows of x behind a sequence are
+ *                read but reach nothing
+ *   splits       nsplit <= 4 host structs; sum of heads * dim = C; out like x
+ *   state_final  [B,K-1,C] like x: the last K - 1 inputs of each sequence (of state0 and x
+ *                together where it is shorter), or NULL to skip; not state0 itself
+ *   mode         DR_IN_BF16? | CONV_SILU?
+ *
+ * Supported: K in {2,3,4}, dim in {32, 64, 128}; T = 0 copies state0. Sums in fp32, one
+ * rounding per output. Outputs may not alias inputs. Returns DR_OK or a negative status; on
+ * error nothing is launched.
+ */
+int short_conv_fwd(const dr_view* x, const float* weight, const float* bias, const void* state0,
+                   const int* lengths, const conv_split* splits, int nsplit, void* state_final,
+                   float eps, int B, int T, int C, int K, int mode, cudaStream_t stream);
+
+/*
+ * short_conv_step -- one token per sequence: x [B,C] view (sb), splits' outputs [B,heads,dim]
+ * (sb, sh), state [B,K-1,C] read and shifted in place (the oldest row leaves, x enters). The
+ * same arithmetic, in the same order, as short_conv_fwd with T = 1.
+ */
+int short_conv_step(const dr_view* x, const float* weight, const float* bias, void* state,
+                    const conv_split* splits, int nsplit, float eps, int B, int C, int K, int mode,
+                    cudaStream_t stream);
+
+/*
+ * ssm_scan_fwd -- selective state space scan over B*H sequences, fp32 state S [P,N]:
+ *
+ *     delta_t = softplus(dt_t + dt_bias_h) with SSM_DT_SOFTPLUS, else dt_t + dt_bias_h
+ *     S_t = exp(delta_t A_h) S_{t-1} + delta_t x_t B_t^T
+ *     y_t = S_t C_t + D_h x_t
+ *
+ *   x, out   [B,H,T,P] views, bf16 if (mode & DR_IN_BF16) else fp32
+ *   dt       [B,H,T] view of single elements, fp32 or (SSM_DT_BF16) bf16, any strides, aligned
+ *            to its element
+ *   A        [H] fp32; D, dt_bias [H] fp32 or NULL (0)
+ *   Bm, Cm   [B,G,T,N] views like x; head h reads group h / (H / G)
+ *   S0       [B,H,P,N] fp32 or NULL for zeros; S_final the same or NULL to skip; not S0 itself
+ *   lengths  [B] int32 on the device or NULL: tokens of each sequence (clamped to 0..T). Rows
+ *            of out behind a sequence are left as they were, whatever x, dt, Bm and Cm hold
+ *            there; S_final is the state after the last token
+ *   mode     DR_IN_BF16? | SSM_DT_SOFTPLUS? | SSM_DT_BF16? | DR_FORCE_SEQUENTIAL?
+ *
+ * Supported: P, N in {32, 64, 128}, H a multiple of G. The steps decay: delta A <= 0 (growth is
+ * computed as written while exp stays finite). Sequences too few to fill the GPU are cut into
+ * segments, whose states take B*H*(segments-1)*(P*N+1) floats of scratch from the library's
+ * stream-ordered pool (DR_ERR_CUDA if it cannot be had); the result is that of the uncut scan
+ * up to fp32 rounding. T = 0 copies S0. out may not alias an input. Returns DR_OK or a negative
+ * status; on error nothing is launched.
+ */
+int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_view* Bm,
+                 const dr_view* Cm, const float* D, const float* dt_bias, const float* S0,
+                 const int* lengths, const dr_view* out, float* S_final, int B, int H, int G,
+                 int T, int P, int N, int mode, cudaStream_t stream);
+
+/*
+ * ssm_step -- one token of the same recurrence on a resident state: S [B,H,P,N] fp32 is read
+ * and updated in place. x, out [B,H,P], dt [B,H], Bm, Cm [B,G,N] views (st not used). Reads and
+ * writes S once. Same rules and return values as ssm_scan_fwd with T = 1.
+ */
+int ssm_step(const dr_view* x, const dr_view* dt, const float* A, const dr_view* Bm,
+             const dr_view* Cm, const float* D, const float* dt_bias, float* S,
+             const dr_view* out, int B, int H, int G, int P, int N, int mode,
+             cudaStream_t stream);
+
+/*
+ * gated_norm_fwd -- RMS norm of a scan's output with its gate, head-major to token-major. Over
+ * groups of norm_heads neighbouring heads, W = norm_heads * d channels, act = silu or sigmoid:
+ *
+ *     out = y / sqrt(mean y^2 + eps) weight act(gate)
+ *     out = v / sqrt(mean v^2 + eps) weight,  v = y act(gate)      with NORM_GATE_FIRST
+ *
+ *   y       [B,H,T,d] view, bf16 if (mode & DR_IN_BF16) else fp32
+ *   gate    [B,T,H d] view like y (sb, st), or NULL (or NULL data): no gate
+ *   weight  [H d] fp32, or [d] with NORM_SHARED_WEIGHT
+ *   out     [B,T,H d] view like y (sb, st)
+ *   mode    DR_IN_BF16? | NORM_SIGMOID? | NORM_GATE_FIRST? | NORM_SHARED_WEIGHT?
+ *
+ * Supported: d in {32, 64, 128}, W <= 16384 (bf16) or 8192 (fp32). Statistics in fp32, one
+ * rounding per output. out may not alias y; it may be gate itself, with the same strides.
+ */
+int gated_norm_fwd(const dr_view* y, const dr_view* gate, const float* weight, const dr_view* out,
+                   float eps, int B, int H, int T, int d, int norm_heads, int mode,
+                   cudaStream_t stream);
+
+/*
+ * block_norm_fwd -- between two blocks, per row of D channels:
+ *
+ *     z = x, or with post_weight  x / sqrt(mean x^2 + eps) post_weight
+ *     r = residual + scale z                  (scale_v [D] if given, else the number scale)
+ *     out = r / sqrt(mean r^2 + eps) weight
+ *
+ *   x             [rows,D], x_pitch elements from row to row; bf16 if (mode & DR_IN_BF16)
+ *   residual      [rows,D] contiguous, like x or (NORM_RESIDUAL_F32) fp32; NULL for zeros
+ *   weight, post_weight, scale_v  [D] fp32; the last two may be NULL
+ *   out           [rows,D] contiguous, like x; may be x itself if x_pitch = D
+ *   residual_out  r, like residual; NULL to skip; may be residual itself
+ *
+ * Supported: D a multiple of 8 (bf16) or 4 (fp32), at most 16384 or 8192. The statistics of r
+ * are of its fp32 values, before they are rounded into residual_out.
+ */
+int block_norm_fwd(const void* x, long long x_pitch, const void* residual, const float* weight,
+                   const float* post_weight, const float* scale_v, float scale, void* out,
+                   void* residual_out, float eps, long long rows, int D, int mode,
+                   cudaStream_t stream);
 
 /* Static, human-readable text for a status code (never NULL). */
 const char* dr_status_string(int status);
