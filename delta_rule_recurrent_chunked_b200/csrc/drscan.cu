@@ -711,6 +711,9 @@ int dr_poll_error(cudaStream_t stream) {
         const int zero = 0;
         if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return DR_ERR_CUDA;
     }
+    int layer = 0;
+    if (layer_poll_status(&layer) != DR_OK) return DR_ERR_CUDA;
+    if (status == 0) status = layer;
     return status;
 }
 

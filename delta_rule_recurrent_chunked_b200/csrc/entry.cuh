@@ -30,5 +30,7 @@ inline int copy_state(float* dst, const float* src, size_t count, cudaStream_t s
 
 // Defined in drscan.cu.
 int scratch_alloc(void** p, size_t bytes, cudaStream_t stream);
+// Defined in layer.cu: reads and clears the status word of that unit's kernels.
+int layer_poll_status(int* status);
 
 }  // namespace drscan

@@ -7,6 +7,7 @@
 #include "entry.cuh"
 #include "norms.cuh"
 #include "short_conv.cuh"
+#include "ssm_chunked.cuh"
 #include "ssm_scan.cuh"
 
 using namespace drscan;
@@ -132,10 +133,7 @@ int launch_ssm_sequential(const SsmArgs& a, cudaStream_t stream) {
             <<<dim3((unsigned)gx, (unsigned)(a.nseg - 1)), SSM_THREADS, 0, stream>>>(a);
         int rc = launch_status();
         if (rc != DR_OK) return rc;
-        const long PN = (long)a.P * a.N, n = (long)a.B * a.H * PN / 4;
-        ssm_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
-            a.seg_state, a.seg_log, (long)a.B * a.H, a.nseg - 1, PN);
-        rc = launch_status();
+        rc = launch_ssm_chain(a, stream);
         if (rc != DR_OK) return rc;
     }
     ssm_sequential_kernel<T, N, SSM_PASS_OUTPUTS>
@@ -189,6 +187,15 @@ int dispatch_ssm_step(const SsmArgs& a, float* S, cudaStream_t stream) {
             return launch_ssm_step<T, 128>(a, S, stream);
     }
     return DR_ERR_UNSUPPORTED;
+}
+
+// SMs of the current device.
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 148;
+    return n;
 }
 
 SsmView as_view(const dr_view* v) {
@@ -281,6 +288,16 @@ struct BlockLaunch {
 
 }  // namespace
 
+// This unit's status word (see dr_poll_error), cleared when read.
+int drscan::layer_poll_status(int* status) {
+    *status = 0;
+    if (cudaMemcpyFromSymbol(status, g_status, sizeof(int)) != cudaSuccess) return DR_ERR_CUDA;
+    const int zero = 0;
+    if (*status != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess)
+        return DR_ERR_CUDA;
+    return DR_OK;
+}
+
 extern "C" {
 
 int short_conv_fwd(const dr_view* x, const float* weight, const float* bias, const void* state0,
@@ -339,7 +356,12 @@ int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_v
     a.S0 = S0;
     a.S_final = S_final;
     a.lengths = lengths;
-    plan_ssm_sequential(&a);
+    const bool chunked =
+        (mode & DR_IN_BF16) && !(mode & DR_FORCE_SEQUENTIAL) && ssm_chunked_fits(a);
+    if (chunked)
+        plan_ssm_chunked(&a, sm_count());
+    else
+        plan_ssm_sequential(&a);
     void* scratch = nullptr;
     if (a.nseg > 1) {
         const size_t states = (size_t)BH * (a.nseg - 1);
@@ -348,8 +370,9 @@ int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_v
         a.seg_state = static_cast<float*>(scratch);
         a.seg_log = a.seg_state + states * PN;
     }
-    rc = (mode & DR_IN_BF16) ? dispatch_ssm_sequential<__nv_bfloat16>(a, stream)
-                             : dispatch_ssm_sequential<float>(a, stream);
+    rc = chunked               ? launch_ssm_chunked(a, stream)
+         : (mode & DR_IN_BF16) ? dispatch_ssm_sequential<__nv_bfloat16>(a, stream)
+                               : dispatch_ssm_sequential<float>(a, stream);
     if (scratch && cudaFreeAsync(scratch, stream) != cudaSuccess && rc == DR_OK) rc = DR_ERR_CUDA;
     return rc;
 }

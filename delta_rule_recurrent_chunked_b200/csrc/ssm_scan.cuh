@@ -209,6 +209,13 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(float* state, const floa
     }
 }
 
+inline int launch_ssm_chain(const SsmArgs& a, cudaStream_t stream) {
+    const long PN = (long)a.P * a.N, n = (long)a.B * a.H * PN / 4;
+    ssm_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+        a.seg_state, a.seg_log, (long)a.B * a.H, a.nseg - 1, PN);
+    return cudaGetLastError() == cudaSuccess ? DR_OK : DR_ERR_CUDA;
+}
+
 // One token on a resident state: S is read and written once, which bounds the step (8 P N bytes
 // a head). A row of S is N / 4 lanes of 16 bytes, so a warp's access covers 128 / N rows in one
 // 512-byte piece; each warp owns SSM_STEP_U such pieces, all loaded before the first is used.
