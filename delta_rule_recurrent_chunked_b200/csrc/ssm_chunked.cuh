@@ -23,10 +23,12 @@
 // exp(g_i - g_end(J)) exp(g_end(J) - g_j), both <= 1: one exponential per row and block and one
 // per token instead of one per element; only the diagonal 32 x 32 blocks take one per element.
 //
-// Roles (576 threads): warps 0-3 weigh the scores (P), 4-7 scale x, 8-11 carry the state, 12-15
-// write the outputs, warp 16 loads tiles by TMA and prepares the per-token factors, warp 17
-// issues the MMAs. Tiles are double-buffered; scores run one chunk ahead, so the only serial
-// dependence between chunks is state -> registers -> S copy -> inter. Every wait is bounded.
+// Roles (1024 threads): warps 0-7 weigh the scores (P), 8-11 scale x, 12-15 carry the state, 16-23
+// write the outputs, warp 24 loads the tiles by TMA, warp 26 issues the scores' MMAs and warp 25
+// all others, warps 28-31 prepare the per-token factors, up to four chunks ahead.
+// Tiles are double-buffered, those of x apart from C and B, which are free as soon as the
+// products have read them; scores run ahead, so the only serial dependence between chunks is
+// state -> registers -> S copy -> inter. Every wait is bounded.
 #pragma once
 
 #include <cuda.h>
@@ -38,7 +40,13 @@ namespace drscan {
 
 constexpr int SCK = 128;        // tokens per chunk
 constexpr int SCV = 64;         // value channels per CTA
-constexpr int SC_THREADS = 576;
+constexpr int SC_THREADS = 1024;
+// Registers per thread: 64 at launch, then by role; the eight groups of four warps hold 2 x 56 (P)
+// + 88 (scaled x) + 112 (state) + 2 x 56 (outputs) + 40 (loads and MMAs) + 48 (factors) = 8 x 64.
+constexpr int SC_REG_P = 56, SC_REG_X = 88, SC_REG_STATE = 112, SC_REG_OUT = 56,
+              SC_REG_ISSUE = 40, SC_REG_PAR = 48;
+constexpr int SC_AHEAD = 2;     // chunks between a tile's prefetch into L2 and its load
+constexpr int SC_NPAR = 4;      // chunks of per-token factors
 
 // Shared memory (bytes). A tile row is 128 bytes (64 bf16) of a 128-byte-swizzled panel.
 constexpr int SC_PANEL = SCK * 128;                      // 128 rows x 64 channels
@@ -48,7 +56,7 @@ constexpr int SC_X = SC_B + 2 * SC_PANEL;                // one panel
 constexpr int SC_STAGE = SC_X + SC_PANEL;
 constexpr int SC_XS = 2 * SC_STAGE;                      // xh, xl panels
 constexpr int SC_S = SC_XS + 2 * SC_PANEL;               // S^T rows n, 64 value channels
-constexpr int SC_PAR = SC_S + SC_PANEL;                  // [stage] SsmChunkPar
+constexpr int SC_PAR = SC_S + SC_PANEL;                  // [SC_NPAR] SsmChunkPar
 struct SsmChunkPar {
     float g2[SCK];     // g_i log2(e)
     float delta[SCK];
@@ -58,22 +66,31 @@ struct SsmChunkPar {
     float gamma;       // exp(g_Q)
     float pad[3];
 };
-constexpr int SC_BAR = SC_PAR + 2 * (int)sizeof(SsmChunkPar);
+constexpr int SC_BAR = SC_PAR + SC_NPAR * (int)sizeof(SsmChunkPar);
+// Barriers. One that is waited for by a role which may lag behind the next phase (its other
+// waiters alone let that one complete) exists twice, for even and odd chunks: a wait by parity
+// tells neighbouring phases apart, not a phase from the one after the next.
 enum {
-    SB_FULL = 0,     // [2] tiles and factors of a stage are there
-    SB_FREE = 2,     // [2] .. may be overwritten
-    SB_SCORE = 4,    // [2] scores are in tensor memory
-    SB_P = 6,        // [2] P is in tensor memory
-    SB_XS = 8,       // scaled x is in shared memory
-    SB_DS = 9,       // the chunk's state product is in tensor memory
-    SB_ST = 10,      // the entering state's copy is in shared memory (and the product read)
-    SB_Y = 11,       // inter and intra products are in tensor memory
-    SB_YFREE = 12,   // .. have been read
-    SB_COUNT = 13
+    SB_CB = 0,       // [2] tiles of C and B are there
+    SB_CBFREE = 2,   // [2] .. have been read by their three products
+    SB_X = 4,        // [2] the tile of x is there
+    SB_XFREE = 6,    // [2] .. has been read
+    SB_PAR = 8,      // [SC_NPAR] factors are there
+    SB_PARFREE = 12, // [SC_NPAR]
+    SB_SCORE = 16,   // [2] scores are in tensor memory
+    SB_P = 18,       // [2] P is in tensor memory
+    SB_XS = 20,      // [2] scaled x is in shared memory
+    SB_Y = 22,       // [2] inter and intra products are in tensor memory
+    SB_DS = 24,      // the chunk's state product is in tensor memory
+    SB_DSFREE = 25,  // .. has been read
+    SB_ST = 26,      // the entering state's copy is in shared memory
+    SB_YFREE = 27,   // inter and intra products have been read
+    SB_DRAIN = 28,   // [3] after a timeout
+    SB_COUNT = 31
 };
-constexpr int SC_TOTAL = SC_BAR + 8 * SB_COUNT + 24;
+constexpr int SC_TOTAL = SC_BAR + 8 * SB_COUNT + 32;
 // Tensor memory columns
-constexpr uint32_t TC_SCORE = 0;   // [2] 128 columns; P in the first 64
+constexpr uint32_t TC_SCORE = 0;   // [2] 128 columns; of each 16, P takes the first 8
 constexpr uint32_t TC_INTRA = 256, TC_INTER = 320, TC_DS = 384;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -81,6 +98,35 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+// The two bf16 of a word, and back.
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) { return pack_bf16(x.x, x.y); }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int c0,
                                             int c1, int c2, int c3) {
@@ -91,15 +137,120 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint3
         : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T: A packs two bf16 of K in a 32-bit column. One thread.
-__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
+// MMA and commit issued by one elected lane of a converged warp. With every operand the same in
+// all lanes (and unrolled) the descriptors stay in uniform registers: an N = 128 product then
+// issues every 64 cycles, the tensor core's rate; from a divergent lane, with descriptors formed
+// in a loop, the same instruction measured about 190.
+// D[tmem] (+)= A[smem] * B[smem]^T
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: A packs two bf16 of K in a 32-bit column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// The product of K = kdim with A a tile along K (panels of 64, from shared address `a`) and B from
+// descriptor `db`, which grows by `bstep` a K step and has `bpanel` from panel to panel.
+__device__ __forceinline__ void mma_kmajor(uint32_t d_tmem, uint32_t a, uint64_t db,
+                                           uint32_t bstep, uint32_t bpanel, int kdim,
+                                           uint32_t idesc) {
+    uint64_t da = smem_desc_sw128(a, 16, 1024);
+    uint32_t acc = 0;
+#pragma unroll 1
+    for (int k = 0; k < kdim; k += 16) {
+        mma_ss(d_tmem, da, db, idesc, acc);
+        acc = 1;
+        const bool turn = (k & 48) == 48;  // the panel's last step
+        da += turn ? (SC_PANEL >> 4) - 6 : 2;
+        db += turn ? bpanel - 3 * bstep : bstep;
+    }
+}
+
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar)
+        : "memory");
+}
+
+// Waits, as a whole warp, for the phase with the given parity: by a vote, since lanes that leave
+// the polls at different times would run what follows one after another. The wait is bounded by
+// its polls (a poll takes some 20 cycles to some microseconds, so 2^20 of them at least 10 ms,
+// a thousand times the longest wait for memory, and seconds at most). False (with the status
+// latched) when they ran out: the caller leaves its loop, and whoever waits for it runs out too.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+    int polls = 1 << 20;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
+        if (--polls == 0) {
+            raise_status(DR_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// 8 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7])
+        : "r"(taddr));
+}
+
+// .. and stored.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* u) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]),
+                 "r"(u[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* u) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+
+// Bits of the pair of elements 0 and 1 of which those up to `top` count.
+__device__ __forceinline__ uint32_t pair_mask(int top) {
+    return top >= 1 ? 0xffffffffu : top == 0 ? 0xffffu : 0u;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A box of a tensor map into L2 only.
+__device__ __forceinline__ void tma_prefetch_4d(const void* map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
 }
 
 // After an abort: waits (bounded) for the async work of a phase that was started.
@@ -113,6 +264,7 @@ struct SsmChunkArgs {
     SsmArgs s;
     // 1 where the tensor map's head / batch coordinate counts, 0 where the view repeats
     int xh, xb, bh, bb, ch, cb;
+    int out32;  // the rows of out lie on 32-byte boundaries
 };
 
 // grid: (B * H * slices of SCV value channels, segments of this pass); block: SC_THREADS.
@@ -126,15 +278,28 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SC_BAR);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + SC_BAR + 8 * SB_COUNT);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sm + SC_BAR + 8 * SB_COUNT + 8);
+    float* sums = reinterpret_cast<float*>(sm + SC_BAR + 8 * SB_COUNT + 16);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto stage = [&](int s) { return sm + s * SC_STAGE; };
     auto par = [&](int s) {
         return reinterpret_cast<SsmChunkPar*>(sm + SC_PAR + s * (int)sizeof(SsmChunkPar));
     };
+    // waits of chunk c
+    auto wait2 = [&](int i, int c) {
+        return mbar_wait_warp(bar(i + (c & 1)), (uint32_t)((c >> 1) & 1));
+    };
+    auto wait1 = [&](int i, int c) {
+        return mbar_wait_warp(bar(i), (uint32_t)(c & 1));
+    };
+    auto wait_par = [&](int c) {
+        return mbar_wait_warp(bar(SB_PAR + c % SC_NPAR), (uint32_t)((c / SC_NPAR) & 1));
+    };
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (by a shuffle, so that the compiler knows the roles' branches to be uniform: without it the
+    // two issuing warps' code is more than twice as long)
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int nsl = (a.P + SCV - 1) / SCV;
     const int v0 = (int)(blockIdx.x % nsl) * SCV;
     const long bh = blockIdx.x / nsl;
@@ -145,78 +310,123 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
     const int t0 = seg * a.seg_len;
     const int ntok = max(0, min(len - t0, min(a.seg_len, a.T - t0)));
-    const int nc = (ntok + SCK - 1) / SCK;
+    int nc = (ntok + SCK - 1) / SCK;
     auto valid = [&](int c) { return min(SCK, ntok - c * SCK); };
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(SB_FULL + s), 2);
-            mbar_init(bar(SB_FREE + s), OUT ? 16 : 8);  // warps of the roles that read a stage
+            mbar_init(bar(SB_CB + s), 1);
+            mbar_init(bar(SB_CBFREE + s), OUT ? 3 : 1);  // the scores, the state's, the inter product
+            mbar_init(bar(SB_X + s), 1);
+            mbar_init(bar(SB_XFREE + s), OUT ? 9 : 4);  // the intra product and the output warps; the scaling warps
             mbar_init(bar(SB_SCORE + s), 1);
-            mbar_init(bar(SB_P + s), 128);
+            mbar_init(bar(SB_P + s), 256);
+            mbar_init(bar(SB_Y + s), 1);
+            mbar_init(bar(SB_XS + s), 128);
         }
-        mbar_init(bar(SB_XS), 128);
+        for (int s = 0; s < SC_NPAR; ++s) {
+            mbar_init(bar(SB_PAR + s), 1);
+            mbar_init(bar(SB_PARFREE + s), OUT ? 24 : 8);  // the warps that read factors
+        }
         mbar_init(bar(SB_DS), 1);
         mbar_init(bar(SB_ST), 128);
-        mbar_init(bar(SB_Y), 1);
-        mbar_init(bar(SB_YFREE), 128);
-        *abort_flag = 0;
+        mbar_init(bar(SB_DSFREE), 128);
+        for (int i = 0; i < 3; ++i) mbar_init(bar(SB_DRAIN + i), 1);
+        mbar_init(bar(SB_YFREE), 256);
         mbar_init_fence();
     }
-    if (warp == 17) tmem_alloc(smem_u32(tmem_holder), 512);
+    if (warp == 25) tmem_alloc(smem_u32(tmem_holder), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    // all 512 columns are this CTA's, so they start at 0: as a constant, addresses of tensor
+    // memory cost the issuing warps nothing
+    constexpr uint32_t tmem = 0;
+    if (*tmem_holder != tmem) {
+        if (tid == 0) raise_status(DR_ERR_DEVICE_BOUNDS);
+        nc = 0;
+    }
     // a warp's 32 lanes of tensor memory
     const uint32_t trow = tmem + ((uint32_t)(warp & 3) << 21);
-    auto release = [&](int s) {  // this warp is done with the stage
-        fence_async_smem();
+    auto release_par = [&](int c) {  // this warp has read the chunk's factors
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(SB_FREE + s));
+        if (lane == 0) mbar_arrive(bar(SB_PARFREE + c % SC_NPAR));
     };
 
-    if (warp == 16) {
-        // ------------------------------------------------------------------ loads and factors
-        const float l2e = 1.4426950408889634f;
-        const float Ah = a.A[h];
-        float logsum = 0.f;
-        float dnext[4];
-        auto fetch = [&](int c) {  // delta of this lane's four tokens, 0 behind the sequence
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int t = c * SCK + 4 * lane + k;
-                dnext[k] = t < ntok ? ssm_delta(a, b, h, (long)t0 + t) : 0.f;
-            }
-        };
-        if (nc > 0) fetch(0);
-        int c = 0;
+    if (warp >= 24 && warp < 28) regs_down<SC_REG_ISSUE>();
+    if (warp == 24) {
+        // ------------------------------------------------------------------ tiles
+        const int np = a.N > 64 ? 2 : 1;
+        int c = 0, loaded_cb = 0;
         for (; c < nc; ++c) {
-            const int s = c & 1;
-            if (c >= 2 && !mbar_wait(bar(SB_FREE + s), (uint32_t)(((c >> 1) - 1) & 1), abort_flag))
-                break;
-            if (lane == 0) {
-                const uint32_t full = bar(SB_FULL + s), base = smem_u32(stage(s));
-                const int np = a.N > 64 ? 2 : 1;
-                mbar_arrive_expect_tx(full, (uint32_t)((OUT ? 2 * np : np) + 1) * SC_PANEL);
+            const uint32_t fx = bar(SB_X + (c & 1)), fcb = bar(SB_CB + (c & 1));
+            const uint32_t base = smem_u32(stage(c & 1));
+            const int t = t0 + c * SCK, ta = t + SC_AHEAD * SCK;
+            if (lane == 0 && c + SC_AHEAD < nc) {
+                tma_prefetch_4d(&tmX, v0, ta, h * ca.xh, (int)b * ca.xb);
+#pragma unroll 1
                 for (int p = 0; p < np; ++p) {
-                    tma_load_4d(base + SC_B + p * SC_PANEL, &tmB, full, 64 * p, t0 + c * SCK,
-                                g * ca.bh, (int)b * ca.bb);
-                    if (OUT)
-                        tma_load_4d(base + SC_C + p * SC_PANEL, &tmC, full, 64 * p, t0 + c * SCK,
-                                    g * ca.ch, (int)b * ca.cb);
+                    tma_prefetch_4d(&tmB, 64 * p, ta, g * ca.bh, (int)b * ca.bb);
+                    if (OUT) tma_prefetch_4d(&tmC, 64 * p, ta, g * ca.ch, (int)b * ca.cb);
                 }
-                tma_load_4d(base + SC_X, &tmX, full, v0, t0 + c * SCK, h * ca.xh, (int)b * ca.xb);
             }
-            float d[4], l[4], pre[4], suf[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) d[k] = dnext[k], l[k] = d[k] * Ah * l2e;
-            if (c + 1 < nc) fetch(c + 1);
-            // inclusive sums from the left, exclusive from the right (short near the chunk's end,
-            // where the weights of the state are largest)
-            pre[0] = l[0], pre[1] = pre[0] + l[1], pre[2] = pre[1] + l[2], pre[3] = pre[2] + l[3];
-            suf[3] = 0.f, suf[2] = l[3], suf[1] = suf[2] + l[2], suf[0] = suf[1] + l[1];
-            float left = pre[3], right = pre[3];
+            __syncwarp();
+            if (c >= 2 && !wait2(SB_CBFREE, c - 2)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(fcb, (uint32_t)(OUT ? 2 * np : np) * SC_PANEL);
+#pragma unroll 1
+                for (int p = 0; p < np; ++p) {
+                    tma_load_4d(base + SC_B + p * SC_PANEL, &tmB, fcb, 64 * p, t, g * ca.bh,
+                                (int)b * ca.bb);
+                    if (OUT)
+                        tma_load_4d(base + SC_C + p * SC_PANEL, &tmC, fcb, 64 * p, t, g * ca.ch,
+                                    (int)b * ca.cb);
+                }
+            }
+            __syncwarp();
+            loaded_cb = c + 1;
+            if (c >= 2 && !wait2(SB_XFREE, c - 2)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(fx, SC_PANEL);
+                tma_load_4d(base + SC_X, &tmX, fx, v0, t, h * ca.xh, (int)b * ca.xb);
+            }
+            __syncwarp();
+        }
+        // a wait ran out: loads in flight may not outlive the CTA
+        if (c < nc) {
+#pragma unroll 1
+            for (int k = max(0, loaded_cb - 2); k < loaded_cb; ++k)
+                mbar_drain(bar(SB_CB + (k & 1)), (uint32_t)((k >> 1) & 1));
+#pragma unroll 1
+            for (int k = max(0, c - 2); k < c; ++k)
+                mbar_drain(bar(SB_X + (k & 1)), (uint32_t)((k >> 1) & 1));
+        }
+    } else if (warp >= 28) {
+        // ------------------------------------------------------------------ per-token factors
+        // (warp 28 + k those of chunks k, k + 4, ..: one warp alone took 6,000 cycles a chunk,
+        // twice what the products need)
+        regs_down<SC_REG_PAR>();
+        const float Ah = a.A[h] * 1.4426950408889634f;  // decays as powers of two
+        float logsum = 0.f;
+        static_assert(SC_NPAR == 4, "a slot of factors per warp");
+        int c = warp - 28;
+        for (; c < nc; c += SC_NPAR) {
+            if (c >= SC_NPAR && !mbar_wait_warp(bar(SB_PARFREE + c % SC_NPAR),
+                                                (uint32_t)((c / SC_NPAR - 1) & 1)))
+                break;
+            SsmChunkPar* pr = par(c % SC_NPAR);
+#pragma unroll 1
+            for (int t = lane; t < SCK; t += 32)  // a step of 0 behind the sequence keeps the state
+                pr->delta[t] = c * SCK + t < ntok
+                                   ? ssm_delta(a, h, ssm_dt(a, b, h, (long)t0 + c * SCK + t))
+                                   : 0.f;
+            __syncwarp();
+            // four neighbouring tokens per lane: sums from the chunk's left (inclusive) and right
+            // (exclusive: short near the chunk's end, where the weights of the state are largest)
+            const float4 d = *reinterpret_cast<const float4*>(&pr->delta[4 * lane]);
+            const float l0 = d.x * Ah, l1 = d.y * Ah, l2 = d.z * Ah, l3 = d.w * Ah;
+            const float q1 = l0 + l1, q2 = q1 + l2, q3 = q2 + l3;
+            float left = q3, right = q3;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const float x = __shfl_up_sync(0xffffffffu, left, off);
@@ -227,318 +437,354 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             const float total = __shfl_sync(0xffffffffu, left, 31);
             float lx = __shfl_up_sync(0xffffffffu, left, 1);
             float rx = __shfl_down_sync(0xffffffffu, right, 1);
-            lx = lane == 0 ? 0.f : lx;
-            rx = lane == 31 ? 0.f : rx;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) pre[k] += lx, suf[k] += rx;
-            const float end = __shfl_sync(0xffffffffu, pre[3], lane | 7);  // of the block of 32
-            SsmChunkPar* pr = par(s);
-            *reinterpret_cast<float4*>(&pr->g2[4 * lane]) = make_float4(pre[0], pre[1], pre[2], pre[3]);
-            *reinterpret_cast<float4*>(&pr->delta[4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+            if (lane == 0) lx = 0.f;
+            if (lane == 31) rx = 0.f;
+            const float4 gp = make_float4(lx + l0, lx + q1, lx + q2, lx + q3);
+            const float end = __shfl_sync(0xffffffffu, gp.w, lane | 7);  // of the block of 32
+            *reinterpret_cast<float4*>(&pr->g2[4 * lane]) = gp;
             *reinterpret_cast<float4*>(&pr->u[4 * lane]) =
-                make_float4(d[0] * ex2(end - pre[0]), d[1] * ex2(end - pre[1]),
-                            d[2] * ex2(end - pre[2]), d[3] * ex2(end - pre[3]));
+                make_float4(d.x * ex2(end - gp.x), d.y * ex2(end - gp.y), d.z * ex2(end - gp.z),
+                            d.w * ex2(end - gp.w));
             *reinterpret_cast<float4*>(&pr->w[4 * lane]) =
-                make_float4(d[0] * exp2f(suf[0]), d[1] * exp2f(suf[1]), d[2] * exp2f(suf[2]),
-                            d[3] * exp2f(suf[3]));
+                make_float4(d.x * ex2(rx + l1 + l2 + l3), d.y * ex2(rx + l2 + l3),
+                            d.z * ex2(rx + l3), d.w * ex2(rx));
             *reinterpret_cast<float4*>(&pr->eg[4 * lane]) =
-                make_float4(ex2(pre[0]), ex2(pre[1]), ex2(pre[2]), ex2(pre[3]));
-            if (lane == 0) pr->gamma = exp2f(total);
+                make_float4(ex2(gp.x), ex2(gp.y), ex2(gp.z), ex2(gp.w));
+            if (lane == 0) pr->gamma = ex2(total);
             logsum += total;
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(SB_FULL + s));
+            if (lane == 0) mbar_arrive(bar(SB_PAR + c % SC_NPAR));
         }
-        if (!OUT && lane == 0 && v0 == 0)
-            a.seg_log[bh * (a.nseg - 1) + seg] = logsum * 0.6931471805599453f;
-        if (*abort_flag) {  // loads in flight may not outlive the CTA
-            for (int k = max(0, c - 2); k < c; ++k)
-                mbar_drain(bar(SB_FULL + (k & 1)), (uint32_t)((k >> 1) & 1));
-        }
-    } else if (warp == 17) {
-        // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_score = idesc_bf16(128, 128, 0, 0);
-            constexpr uint32_t id_val = idesc_bf16(128, 64, 0, 1);
-            constexpr uint32_t id_state = idesc_bf16(128, 128, 1, 1);
-            const int ksteps = a.N / 16;
-            const uint32_t ss = smem_u32(sm + SC_S), xs = smem_u32(sm + SC_XS);
-            auto scores = [&](int c) {
-                const uint32_t st = smem_u32(stage(c & 1));
-                for (int kk = 0; kk < ksteps; ++kk) {
-                    const uint32_t o = (kk >> 2) * SC_PANEL + (kk & 3) * 32;
-                    tc_mma_bf16(tmem + TC_SCORE + 128 * (c & 1),
-                                smem_desc_sw128(st + SC_C + o, 16, 1024),
-                                smem_desc_sw128(st + SC_B + o, 16, 1024), id_score, kk > 0);
-                }
-                tc_commit(bar(SB_SCORE + (c & 1)));
-            };
-            bool ok = true;
-            int c = 0;
-            if (OUT && nc > 0) {
-                ok = mbar_wait(bar(SB_FULL), 0, abort_flag);
-                if (ok) scores(0);
+        // the warps' sums, in a fixed order, at the end of the kernel
+        if (!OUT && lane == 0) sums[warp - 28] = logsum;
+    } else if (warp >= 25 && warp < 28) {
+        // ------------------------------------------------------------------ MMAs
+        // (whole warps, converged: see mma_ss. Three of them, so that no product waits for what
+        // another waits for; each K step in a loop, whose few instructions stay in the first
+        // instruction cache)
+        const uint32_t base = smem_u32(sm);
+        const int n = (int)__reduce_max_sync(0xffffffffu, (unsigned)nc);
+        int c = 0;
+        if (warp == 26) {
+            // scores, as early as their tiles and the place of the P before last allow
+            for (; OUT && c < n; ++c) {
+                if (!wait2(SB_CB, c)) break;
+                if (c >= 2 && !wait2(SB_Y, c - 2)) break;
+                const uint32_t st = base + (c & 1) * SC_STAGE;
+                mma_kmajor(tmem + TC_SCORE + 128 * (c & 1), st + SC_C,
+                           smem_desc_sw128(st + SC_B, 16, 1024), 2, SC_PANEL >> 4, a.N,
+                           idesc_bf16(128, 128, 0, 0));
+                commit_elected(bar(SB_SCORE + (c & 1)));
+                commit_elected(bar(SB_CBFREE + (c & 1)));
             }
-            for (; ok && c < nc; ++c) {
-                const int s = c & 1;
-                const uint32_t st = smem_u32(stage(s));
-                if (OUT && c + 1 < nc) {
-                    // the next chunk's scores, where the chunk before had its P
-                    ok = mbar_wait(bar(SB_FULL + (s ^ 1)), (uint32_t)(((c + 1) >> 1) & 1),
-                                   abort_flag) &&
-                         (c == 0 || mbar_wait(bar(SB_Y), (uint32_t)((c - 1) & 1), abort_flag));
-                    if (!ok) break;
-                    scores(c + 1);
-                }
-                if (!OUT && !(ok = mbar_wait(bar(SB_FULL + s), (uint32_t)((c >> 1) & 1), abort_flag)))
-                    break;
-                if (!(ok = mbar_wait(bar(SB_ST), (uint32_t)(c & 1), abort_flag))) break;
+        } else if (warp == 25) {
+            // the state's
+            for (; c < n; ++c) {
+                if (!wait2(SB_CB, c)) break;
+                if (!wait2(SB_XS, c)) break;
+                if (c > 0 && !wait1(SB_DSFREE, c - 1)) break;
                 tc_fence_after();
-                if (OUT) {
-                    if (c > 0 &&
-                        !(ok = mbar_wait(bar(SB_YFREE), (uint32_t)((c - 1) & 1), abort_flag)))
-                        break;
-                    tc_fence_after();
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        tc_mma_bf16(tmem + TC_INTER,
-                                    smem_desc_sw128(st + SC_C + (kk >> 2) * SC_PANEL + (kk & 3) * 32,
-                                                    16, 1024),
-                                    smem_desc_sw128(ss + kk * 2048, SC_PANEL, 1024), id_val, kk > 0);
-                }
-                // scaled x is waited for before the intra product too: its writers clear the rows
-                // of x and B behind a sequence
-                ok = mbar_wait(bar(SB_XS), (uint32_t)(c & 1), abort_flag);
-                if (!ok) break;
-                if (OUT) {
-                    if (!(ok = mbar_wait(bar(SB_P + s), (uint32_t)((c >> 1) & 1), abort_flag))) break;
-                    tc_fence_after();
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc_mma_bf16_ta(tmem + TC_INTRA, tmem + TC_SCORE + 128 * s + 8 * kk,
-                                       smem_desc_sw128(st + SC_X + kk * 2048, SC_PANEL, 1024),
-                                       id_val, kk > 0);
-                    tc_commit(bar(SB_Y));
-                }
-                for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_bf16(tmem + TC_DS, smem_desc_sw128(st + SC_B + kk * 2048, SC_PANEL, 1024),
-                                smem_desc_sw128(xs + kk * 2048, SC_PANEL, 1024), id_state, kk > 0);
-                tc_commit(bar(SB_DS));
+                uint64_t da = smem_desc_sw128(base + (c & 1) * SC_STAGE + SC_B, SC_PANEL, 1024);
+                uint64_t db = smem_desc_sw128(base + SC_XS, SC_PANEL, 1024);
+#pragma unroll 1
+                for (uint32_t kk = 0; kk < 8; ++kk, da += 128, db += 128)
+                    mma_ss(tmem + TC_DS, da, db, idesc_bf16(128, 128, 1, 1), kk);
+                commit_elected(bar(SB_DS));
+                commit_elected(bar(SB_CBFREE + (c & 1)));
             }
-            if (!ok) {  // products in flight may not outlive the CTA's memory
-                tc_commit(bar(SB_DS));
-                mbar_drain(bar(SB_DS), (uint32_t)(c & 1));
+        } else {
+            // the outputs'. (Scaled x is waited for as its writers clear the rows of x behind a
+            // sequence.)
+            for (; OUT && c < n; ++c) {
+                const uint32_t s = c & 1, st = base + s * SC_STAGE;
+                if (!wait1(SB_ST, c)) break;
+                if (!wait2(SB_CB, c)) break;
+                if (c > 0 && !wait1(SB_YFREE, c - 1)) break;
+                tc_fence_after();
+                mma_kmajor(tmem + TC_INTER, st + SC_C,
+                           smem_desc_sw128(base + SC_S, SC_PANEL, 1024), 128, 4 * 128, a.N,
+                           idesc_bf16(128, 64, 0, 1));
+                commit_elected(bar(SB_CBFREE + s));
+                if (!wait2(SB_XS, c)) break;
+                if (!wait2(SB_P, c)) break;
+                tc_fence_after();
+                uint64_t dx = smem_desc_sw128(st + SC_X, SC_PANEL, 1024);
+                uint32_t pa = tmem + TC_SCORE + 128 * s;
+#pragma unroll 1
+                for (uint32_t kk = 0; kk < 8; ++kk, dx += 128, pa += 16)
+                    mma_ts(tmem + TC_INTRA, pa, dx, idesc_bf16(128, 64, 0, 1), kk);
+                commit_elected(bar(SB_Y + s));
+                commit_elected(bar(SB_XFREE + s));
             }
         }
-        __syncwarp();
-    } else if (warp < 4) {
+        if (c < n) {  // a wait ran out: products in flight may not outlive the CTA's memory
+            const uint32_t b0 = bar(SB_DRAIN + warp - 25);
+            commit_elected(b0);
+            mbar_drain(b0, 0);
+        }
+    } else if (warp < 8) {
         // ------------------------------------------------------------------ P from the scores
+        // (two warps per 32 rows: the one weighs columns 0-63, the other 64-127. The P of 16 columns
+        // goes over the first half of their scores, so no warp writes what another reads.)
+        regs_down<SC_REG_P>();
         if constexpr (OUT) {
-            const int i = tid;
+            const int i = tid & 127, rw = warp & 3;
             for (int c = 0; c < nc; ++c) {
                 const int s = c & 1, nv = valid(c);
-                if (!mbar_wait(bar(SB_FULL + s), (uint32_t)((c >> 1) & 1), abort_flag)) break;
-                const SsmChunkPar* pr = par(s);
+                if (!wait_par(c)) break;
+                const SsmChunkPar* pr = par(c % SC_NPAR);
                 const float gi = pr->g2[i];
-                if (!mbar_wait(bar(SB_SCORE + s), (uint32_t)((c >> 1) & 1), abort_flag)) break;
+                if (!wait2(SB_SCORE, c)) break;
                 tc_fence_after();
                 const uint32_t tsc = trow + TC_SCORE + 128 * s;
+                // 16 columns at a time, in a loop, whose code stays in the instruction cache
+                const int left = 64 * (warp >> 2);
 #pragma unroll 1
-                for (int J = 0; J < 4; ++J) {
-                    uint32_t pk[16];
-                    if (J <= warp) {
-                        float x[32];
-                        tmem_ld16(tsc + 32 * J, x);
-                        tmem_ld16(tsc + 32 * J + 16, x + 16);
-                        tmem_wait_ld();
-                        if (J < warp) {
+                for (int j0 = left; j0 < left + 64; j0 += 16) {
+                    const int J = j0 >> 5;
+                    uint32_t pk[8];
+                    if (J <= rw) {
+                        float2 x[8];
+                        tmem_ld16(tsc + j0, reinterpret_cast<float*>(x));
+                        if (J < rw) {
                             const float r = ex2(gi - pr->g2[32 * J + 31]);
+                            const float4* u = reinterpret_cast<const float4*>(pr->u + j0);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 u = *reinterpret_cast<const float4*>(&pr->u[32 * J + j]);
-                                x[j] *= r * u.x, x[j + 1] *= r * u.y;
-                                x[j + 2] *= r * u.z, x[j + 3] *= r * u.w;
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 w = u[e];
+                                x[2 * e] = mul2(mul2(make_float2(r, r), make_float2(w.x, w.y)),
+                                                x[2 * e]);
+                                x[2 * e + 1] = mul2(mul2(make_float2(r, r), make_float2(w.z, w.w)),
+                                                    x[2 * e + 1]);
                             }
                         } else {
-                            // every lane of the warp is in its diagonal block
+                            const float4* gq = reinterpret_cast<const float4*>(pr->g2 + j0);
+                            const float4* dq = reinterpret_cast<const float4*>(pr->delta + j0);
+                            float2 w[8];
 #pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 gj = *reinterpret_cast<const float4*>(&pr->g2[32 * J + j]);
-                                const float4 dj =
-                                    *reinterpret_cast<const float4*>(&pr->delta[32 * J + j]);
-                                x[j] = j <= lane ? x[j] * (dj.x * ex2(gi - gj.x)) : 0.f;
-                                x[j + 1] = j + 1 <= lane ? x[j + 1] * (dj.y * ex2(gi - gj.y)) : 0.f;
-                                x[j + 2] = j + 2 <= lane ? x[j + 2] * (dj.z * ex2(gi - gj.z)) : 0.f;
-                                x[j + 3] = j + 3 <= lane ? x[j + 3] * (dj.w * ex2(gi - gj.w)) : 0.f;
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 gj = gq[e], dj = dq[e];
+                                w[2 * e] = mul2(make_float2(dj.x, dj.y),
+                                                make_float2(ex2(gi - gj.x), ex2(gi - gj.y)));
+                                w[2 * e + 1] = mul2(make_float2(dj.z, dj.w),
+                                                    make_float2(ex2(gi - gj.z), ex2(gi - gj.w)));
                             }
-                        }
-                        if (nv < SCK) {  // whatever lies behind the sequence (NaN too) weighs nothing
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = 32 * J + j < nv ? x[j] : 0.f;
+                            for (int e = 0; e < 8; ++e) x[e] = mul2(x[e], w[e]);
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+                        for (int e = 0; e < 8; ++e) pk[e] = pack2(x[e]);
+                        if (J == rw || nv < SCK) {
+                            // nothing above the diagonal, and nothing behind the sequence: by bits,
+                            // as it may be infinite or NaN
+                            const int top = min(i, nv - 1) - j0;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) pk[e] &= pair_mask(top - 2 * e);
+                        }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) pk[j] = 0;
+                        for (int e = 0; e < 8; ++e) pk[e] = 0;
                     }
-                    // over the scores of columns 16 J ..: read already, by this very lane
-                    tmem_st16(tsc + 16 * J, reinterpret_cast<const float*>(pk));
+                    tmem_st8(tsc + j0, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(SB_P + s));
-                release(s);
+                release_par(c);
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ------------------------------------------------------------------ scaled x
-        const int j = tid - 128;
+        regs_up<SC_REG_X>();
+        const int j = tid & 127;
         for (int c = 0; c < nc; ++c) {
             const int s = c & 1;
-            if (!mbar_wait(bar(SB_FULL + s), (uint32_t)((c >> 1) & 1), abort_flag)) break;
-            const float w = par(s)->w[j];
+            if (!wait_par(c)) break;
+            const float w = par(c % SC_NPAR)->w[j];
+            release_par(c);
+            if (!wait2(SB_X, c)) break;
+            // rows behind a sequence are cleared in the tile of B too, once it is there
+            if (valid(c) < SCK && !wait2(SB_CB, c)) break;
             uint8_t* xr = stage(s) + SC_X + j * 128;
             uint8_t* br = stage(s) + SC_B + j * 128;
             uint8_t* hi = sm + SC_XS + j * 128;
             const bool live = j < valid(c);
-            uint4 raw[8];
+            // 16-byte pieces keep their swizzled places; each lane starts at another one, so that
+            // eight lanes cover all banks
+            const int turn = (j & 7) << 4;
+            uint32_t top[32], rest[32];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) raw[k] = *reinterpret_cast<const uint4*>(xr + k * 16);
-            if (c > 0 && !mbar_wait(bar(SB_DS), (uint32_t)((c - 1) & 1), abort_flag)) break;
-            if (live) {
+            for (int k = 0; k < 8; ++k) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(xr + ((k << 4) ^ turn));
+                const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {  // 16-byte pieces keep their swizzled places
-                    float x[8], rest[8];
-                    Vec16<__nv_bfloat16>::unpack(raw[k], x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] *= w;
-                    const uint4 top = Vec16<__nv_bfloat16>::pack(x);
-                    Vec16<__nv_bfloat16>::unpack(top, rest);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) rest[e] = x[e] - rest[e];
-                    *reinterpret_cast<uint4*>(hi + k * 16) = top;
-                    *reinterpret_cast<uint4*>(hi + SC_PANEL + k * 16) =
-                        Vec16<__nv_bfloat16>::pack(rest);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = mul2(unpack2(r[e]), make_float2(w, w));
+                    top[4 * k + e] = pack2(x);
+                    rest[4 * k + e] =
+                        pack2(fma2(unpack2(top[4 * k + e]), make_float2(-1.f, -1.f), x));
                 }
-            } else {  // nothing behind the sequence may enter a product, not even as 0 * NaN
-                const uint4 z = make_uint4(0, 0, 0, 0);
+            }
+            if (valid(c) < SCK) {  // nothing behind the sequence may enter a product
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    *reinterpret_cast<uint4*>(hi + k * 16) = z;
-                    *reinterpret_cast<uint4*>(hi + SC_PANEL + k * 16) = z;
-                    *reinterpret_cast<uint4*>(xr + k * 16) = z;
-                    *reinterpret_cast<uint4*>(br + k * 16) = z;
-                    *reinterpret_cast<uint4*>(br + SC_PANEL + k * 16) = z;
+                for (int e = 0; e < 32; ++e) top[e] = live ? top[e] : 0u, rest[e] = live ? rest[e] : 0u;
+            }
+            if (c > 0 && !wait1(SB_DS, c - 1)) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                uint8_t* at = hi + ((k << 4) ^ turn);
+                *reinterpret_cast<uint4*>(at) =
+                    make_uint4(top[4 * k], top[4 * k + 1], top[4 * k + 2], top[4 * k + 3]);
+                *reinterpret_cast<uint4*>(at + SC_PANEL) =
+                    make_uint4(rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
+            }
+            if (!live) {  // .. not even as 0 * NaN
+                const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                for (int k = 0; k < 128; k += 16) {
+                    *reinterpret_cast<uint4*>(xr + k) = z;
+                    *reinterpret_cast<uint4*>(br + k) = z;
+                    *reinterpret_cast<uint4*>(br + SC_PANEL + k) = z;
                 }
             }
             fence_async_smem();
-            mbar_arrive(bar(SB_XS));
-            release(s);
+            mbar_arrive(bar(SB_XS + s));
+            if (!OUT) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(SB_XFREE + s));
+            }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------------------------------ the state
-        const int n = tid - 256;
+        regs_up<SC_REG_STATE>();
+        const int n = tid & 127;
         const long PN = (long)a.P * a.N;
         const bool row = n < a.N;
-        float st[SCV];
+        float2 st[SCV / 2];
         const float* enter = nullptr;
         if (seg == 0)
             enter = a.S0 ? a.S0 + bh * PN : nullptr;
         else if (OUT)
             enter = a.seg_state + (bh * (a.nseg - 1) + seg - 1) * PN;
 #pragma unroll
-        for (int p = 0; p < SCV; ++p)
-            st[p] = enter && row && p < pv ? enter[(long)(v0 + p) * a.N + n] : 0.f;
+        for (int p = 0; p < SCV / 2; ++p) st[p] = make_float2(0.f, 0.f);
+        if (enter && row) {
+            const float* e = enter + (long)v0 * a.N + n;
+#pragma unroll
+            for (int p = 0; p < SCV / 2; ++p, e += 2 * a.N)
+                if (p < 16 || pv == SCV) st[p] = make_float2(e[0], e[a.N]);
+        }
         uint8_t* srow = sm + SC_S + n * 128;
         auto copy = [&]() {
             if (OUT) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     *reinterpret_cast<uint4*>(srow + ((k ^ (n & 7)) << 4)) =
-                        Vec16<__nv_bfloat16>::pack(st + 8 * k);
+                        make_uint4(pack2(st[4 * k]), pack2(st[4 * k + 1]), pack2(st[4 * k + 2]),
+                                   pack2(st[4 * k + 3]));
                 fence_async_smem();
+                mbar_arrive(bar(SB_ST));
             }
-            mbar_arrive(bar(SB_ST));
         };
         copy();
         for (int c = 0; c < nc; ++c) {
-            const int s = c & 1;
-            if (!mbar_wait(bar(SB_FULL + s), (uint32_t)((c >> 1) & 1), abort_flag)) break;
-            const float gamma = par(s)->gamma;
-            if (!mbar_wait(bar(SB_DS), (uint32_t)(c & 1), abort_flag)) break;
+            if (!wait_par(c)) break;
+            const float gamma = par(c % SC_NPAR)->gamma;
+            release_par(c);
+            if (!wait1(SB_DS, c)) break;
             tc_fence_after();
 #pragma unroll
-            for (int p = 0; p < SCV; p += 16) {
-                float hi[16], lo[16];
-                tmem_ld16(trow + TC_DS + p, hi);
-                tmem_ld16(trow + TC_DS + SCV + p, lo);
+            for (int p = 0; p < SCV; p += 8) {
+                float2 hi[4], lo[4];
+                tmem_ld8(trow + TC_DS + p, reinterpret_cast<float*>(hi));
+                tmem_ld8(trow + TC_DS + SCV + p, reinterpret_cast<float*>(lo));
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) st[p + k] = fmaf(gamma, st[p + k], hi[k] + lo[k]);
+                for (int k = 0; k < 4; ++k)
+                    st[p / 2 + k] =
+                        fma2(make_float2(gamma, gamma), st[p / 2 + k], add2(hi[k], lo[k]));
             }
             tc_fence_before();
-            if (c + 1 < nc) copy();  // the inter product has read the old copy before SB_DS
-            release(s);
+            mbar_arrive(bar(SB_DSFREE));
+            if (c + 1 < nc) {  // the inter product has to have read the old copy
+                if (OUT && !wait2(SB_Y, c)) break;
+                copy();
+            }
         }
         float* leave = !OUT ? a.seg_state + (bh * (a.nseg - 1) + seg) * PN
                        : seg == a.nseg - 1 && a.S_final ? a.S_final + bh * PN
                                                         : nullptr;
         if (leave && row) {
+            float* e = leave + (long)v0 * a.N + n;
 #pragma unroll
-            for (int p = 0; p < SCV; ++p)
-                if (p < pv) leave[(long)(v0 + p) * a.N + n] = st[p];
+            for (int p = 0; p < SCV / 2; ++p, e += 2 * a.N)
+                if (p < 16 || pv == SCV) e[0] = st[p].x, e[a.N] = st[p].y;
         }
-    } else if (OUT) {
+    } else if (warp < 24) {
         // ------------------------------------------------------------------ outputs
-        const int i = tid - 384;
-        const float Dh = a.D ? a.D[h] : 0.f;
-        __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + b * a.osb + h * a.osh + v0;
-        for (int c = 0; c < nc; ++c) {
-            const int s = c & 1, nv = valid(c);
-            if (!mbar_wait(bar(SB_FULL + s), (uint32_t)((c >> 1) & 1), abort_flag)) break;
-            const float eg = par(s)->eg[i];
-            uint8_t* xt = stage(s) + SC_X;
-            uint8_t* xr = xt + i * 128;
-            if (!mbar_wait(bar(SB_Y), (uint32_t)(c & 1), abort_flag)) break;
-            tc_fence_after();
-#pragma unroll
-            for (int p = 0; p < SCV; p += 32) {
-                float in[32], it[32];
-                tmem_ld16(trow + TC_INTRA + p, in);
-                tmem_ld16(trow + TC_INTRA + p + 16, in + 16);
-                tmem_ld16(trow + TC_INTER + p, it);
-                tmem_ld16(trow + TC_INTER + p + 16, it + 16);
-                tmem_wait_ld();
-                if (p + 32 >= SCV) {
-                    tc_fence_before();
-                    mbar_arrive(bar(SB_YFREE));
-                }
+        // (a thread per token and 32 channels)
+        regs_down<SC_REG_OUT>();
+        if constexpr (OUT) {
+            const int i = tid & 127, p0 = 32 * ((warp >> 2) & 1);
+            const float Dh = a.D ? a.D[h] : 0.f;
+            __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + b * a.osb + h * a.osh +
+                                ((long)t0 + i) * a.ost + v0 + p0;
+            for (int c = 0; c < nc; ++c, op += SCK * a.ost) {
+                if (!wait_par(c)) break;
+                const float eg = par(c % SC_NPAR)->eg[i];
+                release_par(c);
+                if (!wait2(SB_X, c)) break;
+                // x into registers and its tile free before the products are there; outputs take
+                // its place and leave once the products' columns are free
+                const uint8_t* xr = stage(c & 1) + SC_X + i * 128;
+                uint32_t y[16];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint4* at = reinterpret_cast<uint4*>(xr + (((p / 8 + k) ^ (i & 7)) << 4));
-                    float x[8];
-                    Vec16<__nv_bfloat16>::unpack(*at, x);
+                    const uint4 v =
+                        *reinterpret_cast<const uint4*>(xr + ((2 * p0 + 16 * k) ^ ((i & 7) << 4)));
+                    y[4 * k] = v.x, y[4 * k + 1] = v.y, y[4 * k + 2] = v.z, y[4 * k + 3] = v.w;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(SB_XFREE + (c & 1)));
+                if (!wait2(SB_Y, c)) break;
+                tc_fence_after();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = fmaf(Dh, x[e], fmaf(eg, it[8 * k + e], in[8 * k + e]));
-                    *at = Vec16<__nv_bfloat16>::pack(x);  // over x, which no one else reads now
+                for (int k = 0; k < 32; k += 8) {
+                    float2 in[4], it[4];
+                    tmem_ld8(trow + TC_INTRA + p0 + k, reinterpret_cast<float*>(in));
+                    tmem_ld8(trow + TC_INTER + p0 + k, reinterpret_cast<float*>(it));
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[k / 2 + e] = pack2(fma2(make_float2(Dh, Dh), unpack2(y[k / 2 + e]),
+                                                  fma2(make_float2(eg, eg), it[e], in[e])));
+                }
+                tc_fence_before();
+                mbar_arrive(bar(SB_YFREE));
+                if (i < valid(c) && p0 < pv) {
+                    // (a store costs a cycle per row, whatever its width)
+                    if (ca.out32) {
+                        st_global_32(op, y);
+                        st_global_32(op + 16, y + 8);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<uint4*>(op)[k] =
+                                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    }
                 }
             }
-            __syncwarp();
-            // the warp's 32 rows, four at a time, eight lanes of 16 bytes each
-            const int w0 = (warp & 3) * 32, k = lane & 7;
-#pragma unroll
-            for (int r = 0; r < 32; r += 4) {
-                const int ii = w0 + r + (lane >> 3);
-                const uint4 y = *reinterpret_cast<const uint4*>(xt + ii * 128 + ((k ^ (ii & 7)) << 4));
-                if (ii < nv && 8 * k < pv)
-                    *reinterpret_cast<uint4*>(op + ((long)t0 + c * SCK + ii) * a.ost + 8 * k) = y;
-            }
-            release(s);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 17) tmem_dealloc(tmem, 512);
+    if (!OUT && tid == 0 && v0 == 0)
+        a.seg_log[bh * (a.nseg - 1) + seg] =
+            ((sums[0] + sums[1]) + (sums[2] + sums[3])) * 0.6931471805599453f;
+    if (warp == 25) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -632,6 +878,8 @@ inline int launch_ssm_chunked(const SsmArgs& a, cudaStream_t stream) {
         !ssm_map(&mb, a.Bm, a.N, a.T, a.G, a.B, &ca.bh, &ca.bb) ||
         !ssm_map(&mc, a.Cm, a.N, a.T, a.G, a.B, &ca.ch, &ca.cb))
         return DR_ERR_CUDA;
+    const long ostrides = (a.B > 1 ? a.osb : 0) | (a.H > 1 ? a.osh : 0) | (a.T > 1 ? a.ost : 0);
+    ca.out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && (ostrides & 15) == 0;
     const long gx = (long)a.B * a.H * ((a.P + SCV - 1) / SCV);
     if (gx > 0x7fffffffl || a.nseg > 65535) return DR_ERR_UNSUPPORTED;
     if (a.nseg > 1) {

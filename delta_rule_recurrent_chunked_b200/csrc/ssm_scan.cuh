@@ -50,11 +50,15 @@ struct SsmArgs {
 // them from their entering states (all outputs).
 enum { SSM_PASS_STATES = 0, SSM_PASS_OUTPUTS = 1 };
 
-__device__ __forceinline__ float ssm_delta(const SsmArgs& a, long b, int h, long t) {
+// dt of a token, and the step delta it makes.
+__device__ __forceinline__ float ssm_dt(const SsmArgs& a, long b, int h, long t) {
     const long o = b * a.dt.sb + h * a.dt.sh + t * a.dt.st;
-    float d = a.dt_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.dt.p)[o])
-                        : static_cast<const float*>(a.dt.p)[o];
-    if (a.dt_bias) d += a.dt_bias[h];
+    return a.dt_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.dt.p)[o])
+                     : static_cast<const float*>(a.dt.p)[o];
+}
+
+__device__ __forceinline__ float ssm_delta(const SsmArgs& a, int h, float dt) {
+    const float d = a.dt_bias ? dt + a.dt_bias[h] : dt;
     return a.softplus ? softplus_f32(d) : d;
 }
 
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
             for (int i = 0; i < VEC; ++i) sx[t][c + i] = v[i];
         }
         if (tid < n) {
-            const float d = ssm_delta(a, b, h, tt + tid);
+            const float d = ssm_delta(a, h, ssm_dt(a, b, h, tt + tid));
             sdelta[tid] = d;
             sa[tid] = expf(d * Ah);
             logsum += d * Ah;
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(32 * SSM_STEP_WARPS) ssm_step_kernel(
     float x[SSM_STEP_U];
 #pragma unroll
     for (int u = 0; u < SSM_STEP_U; ++u) x[u] = to_f32<T>(xp[u * RPA]);
-    const float delta = ssm_delta(a, b, h, 0);
+    const float delta = ssm_delta(a, h, ssm_dt(a, b, h, 0));
     const float at = expf(delta * a.A[h]), Dh = a.D ? a.D[h] : 0.f;
     T* op = static_cast<T*>(a.out) + b * a.osb + h * a.osh + p0 + sub;
 #pragma unroll
