@@ -51,4 +51,11 @@ __device__ __forceinline__ float softplus_f32(float x) {
     return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }
 
+// e^l, the factor a state decays by. Near 1, where a state remembers thousands of steps, by way of
+// e^l - 1: the exponential's own error there, up to an ulp and mostly to one side, would add up
+// step after step, where the rounded sum's is half an ulp to either.
+__device__ __forceinline__ float decay_f32(float l) {
+    return l > -0.25f ? 1.f + expm1f(l) : expf(l);
+}
+
 }  // namespace drscan

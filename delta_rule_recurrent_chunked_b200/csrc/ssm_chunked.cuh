@@ -11,21 +11,21 @@
 //     scores  C B^T             M=128 N=128 K=N     both from shared memory
 //     inter   C S^T             M=128 N=64  K=N     S as bf16
 //     intra   P x               M=128 N=64  K=128   P (bf16) in tensor memory, over its scores
-//     state   B^T [xh | xl]     M=128 N=128 K=128   xh + xl = exp(g_Q - g_j) delta_j x_j
+//     state   B^T x1, x2, x3    M=128 N=64  K=128   x1 + x2 + x3 = exp(g_Q - g_j) delta_j x_j
 // The state stays in the registers of one warpgroup in fp32 (a lane per row n of S^T).
 //
 // Roundings to bf16, each a choice: P and the copy of S that the outputs read (2^-8 of a
-// product; the outputs are rounded to bf16 themselves), and the scaled x in two halves xh + xl
-// (2^-16: one half alone would put 2^-8 into the state, which is carried on and returned in
-// fp32). x, B and C are bf16 as they come.
+// product; the outputs are rounded to bf16 themselves). The state is carried on and returned in
+// fp32, so the scaled x goes in three bf16 parts of 8 bits each (2^-24; two parts left 2.4e-6 in
+// the state where its fp32 sums leave 2e-7). x, B and C are bf16 as they come.
 //
 // exp(g_i - g_j) for columns of an earlier 32-token block J of the chunk is taken as
 // exp(g_i - g_end(J)) exp(g_end(J) - g_j), both <= 1: one exponential per row and block and one
 // per token instead of one per element; only the diagonal 32 x 32 blocks take one per element.
 //
-// Roles (1024 threads): warps 0-7 weigh the scores (P), 8-11 scale x, 12-15 carry the state, 16-23
-// write the outputs, warp 24 loads the tiles by TMA, warp 26 issues the scores' MMAs and warp 25
-// all others, warps 28-31 prepare the per-token factors, up to four chunks ahead.
+// Roles (1024 threads): warps 0-7 weigh the scores (P), 8-15 scale x, 16-19 carry the state, 20-23
+// write the outputs, warp 24 loads the tiles by TMA, warps 25-27 issue the MMAs of the state, the
+// scores and the outputs, warps 28-31 prepare the per-token factors, up to four chunks ahead.
 // Tiles are double-buffered, those of x apart from C and B, which are free as soon as the
 // products have read them; scores run ahead, so the only serial dependence between chunks is
 // state -> registers -> S copy -> inter. Every wait is bounded.
@@ -42,8 +42,9 @@ constexpr int SCK = 128;        // tokens per chunk
 constexpr int SCV = 64;         // value channels per CTA
 constexpr int SC_THREADS = 1024;
 // Registers per thread: 64 at launch, then by role; the eight groups of four warps hold 2 x 56 (P)
-// + 88 (scaled x) + 112 (state) + 2 x 56 (outputs) + 40 (loads and MMAs) + 48 (factors) = 8 x 64.
-constexpr int SC_REG_P = 56, SC_REG_X = 88, SC_REG_STATE = 112, SC_REG_OUT = 56,
+// + 2 x 56 (scaled x) + 112 (state) + 80 (outputs) + 40 (loads and MMAs) + 48 (factors), not more
+// than 8 x 64.
+constexpr int SC_REG_P = 56, SC_REG_X = 56, SC_REG_STATE = 112, SC_REG_OUT = 80,
               SC_REG_ISSUE = 40, SC_REG_PAR = 48;
 constexpr int SC_AHEAD = 2;     // chunks between a tile's prefetch into L2 and its load
 constexpr int SC_NPAR = 4;      // chunks of per-token factors
@@ -54,8 +55,10 @@ constexpr int SC_C = 0;                                  // [stage] two panels
 constexpr int SC_B = SC_C + 2 * SC_PANEL;                // two panels
 constexpr int SC_X = SC_B + 2 * SC_PANEL;                // one panel
 constexpr int SC_STAGE = SC_X + SC_PANEL;
-constexpr int SC_XS = 2 * SC_STAGE;                      // xh, xl panels
-constexpr int SC_S = SC_XS + 2 * SC_PANEL;               // S^T rows n, 64 value channels
+constexpr int SC_NXS = 3;                                // slots of scaled x, 32 tokens each
+constexpr int SC_XPART = 32 * 128;                       // .. of three parts
+constexpr int SC_XS = 2 * SC_STAGE;
+constexpr int SC_S = SC_XS + SC_NXS * 3 * SC_XPART;      // S^T rows n, 64 value channels
 constexpr int SC_PAR = SC_S + SC_PANEL;                  // [SC_NPAR] SsmChunkPar
 struct SsmChunkPar {
     float g2[SCK];     // g_i log2(e)
@@ -79,19 +82,22 @@ enum {
     SB_PARFREE = 12, // [SC_NPAR]
     SB_SCORE = 16,   // [2] scores are in tensor memory
     SB_P = 18,       // [2] P is in tensor memory
-    SB_XS = 20,      // [2] scaled x is in shared memory
+    SB_CLEAR = 20,   // [2] the tile of x holds nothing behind the sequence
     SB_Y = 22,       // [2] inter and intra products are in tensor memory
     SB_DS = 24,      // the chunk's state product is in tensor memory
     SB_DSFREE = 25,  // .. has been read
     SB_ST = 26,      // the entering state's copy is in shared memory
     SB_YFREE = 27,   // inter and intra products have been read
-    SB_DRAIN = 28,   // [3] after a timeout
-    SB_COUNT = 31
+    SB_XS = 28,      // [SC_NXS] scaled x of 32 tokens is in its slot
+    SB_XSFREE = 31,  // [4] .. of the chunk's quarter has been read
+    SB_DRAIN = 35,   // [3] after a timeout
+    SB_COUNT = 38
 };
 constexpr int SC_TOTAL = SC_BAR + 8 * SB_COUNT + 32;
 // Tensor memory columns
 constexpr uint32_t TC_SCORE = 0;   // [2] 128 columns; of each 16, P takes the first 8
-constexpr uint32_t TC_INTRA = 256, TC_INTER = 320, TC_DS = 384;
+constexpr uint32_t TC_INTRA = 256, TC_INTER = 320;
+constexpr uint32_t TC_DS = 384;    // 64 columns of the first parts, 64 of the others
 
 __device__ __forceinline__ float ex2(float x) {
     float r;
@@ -318,21 +324,23 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             mbar_init(bar(SB_CB + s), 1);
             mbar_init(bar(SB_CBFREE + s), OUT ? 3 : 1);  // the scores, the state's, the inter product
             mbar_init(bar(SB_X + s), 1);
-            mbar_init(bar(SB_XFREE + s), OUT ? 9 : 4);  // the intra product and the output warps; the scaling warps
+            mbar_init(bar(SB_XFREE + s), OUT ? 5 : 8);  // the intra product and the output warps; the scaling warps
             mbar_init(bar(SB_SCORE + s), 1);
             mbar_init(bar(SB_P + s), 256);
             mbar_init(bar(SB_Y + s), 1);
-            mbar_init(bar(SB_XS + s), 128);
+            mbar_init(bar(SB_CLEAR + s), 8);
         }
         for (int s = 0; s < SC_NPAR; ++s) {
             mbar_init(bar(SB_PAR + s), 1);
-            mbar_init(bar(SB_PARFREE + s), OUT ? 24 : 8);  // the warps that read factors
+            mbar_init(bar(SB_PARFREE + s), OUT ? 24 : 12);  // the warps that read factors
         }
         mbar_init(bar(SB_DS), 1);
         mbar_init(bar(SB_ST), 128);
         mbar_init(bar(SB_DSFREE), 128);
+        for (int i = 0; i < SC_NXS; ++i) mbar_init(bar(SB_XS + i), 2);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(SB_XSFREE + i), 1);
         for (int i = 0; i < 3; ++i) mbar_init(bar(SB_DRAIN + i), 1);
-        mbar_init(bar(SB_YFREE), 256);
+        mbar_init(bar(SB_YFREE), 128);
         mbar_init_fence();
     }
     if (warp == 25) tmem_alloc(smem_u32(tmem_holder), 512);
@@ -353,55 +361,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
         if (lane == 0) mbar_arrive(bar(SB_PARFREE + c % SC_NPAR));
     };
 
-    if (warp >= 24 && warp < 28) regs_down<SC_REG_ISSUE>();
-    if (warp == 24) {
-        // ------------------------------------------------------------------ tiles
-        const int np = a.N > 64 ? 2 : 1;
-        int c = 0, loaded_cb = 0;
-        for (; c < nc; ++c) {
-            const uint32_t fx = bar(SB_X + (c & 1)), fcb = bar(SB_CB + (c & 1));
-            const uint32_t base = smem_u32(stage(c & 1));
-            const int t = t0 + c * SCK, ta = t + SC_AHEAD * SCK;
-            if (lane == 0 && c + SC_AHEAD < nc) {
-                tma_prefetch_4d(&tmX, v0, ta, h * ca.xh, (int)b * ca.xb);
-#pragma unroll 1
-                for (int p = 0; p < np; ++p) {
-                    tma_prefetch_4d(&tmB, 64 * p, ta, g * ca.bh, (int)b * ca.bb);
-                    if (OUT) tma_prefetch_4d(&tmC, 64 * p, ta, g * ca.ch, (int)b * ca.cb);
-                }
-            }
-            __syncwarp();
-            if (c >= 2 && !wait2(SB_CBFREE, c - 2)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(fcb, (uint32_t)(OUT ? 2 * np : np) * SC_PANEL);
-#pragma unroll 1
-                for (int p = 0; p < np; ++p) {
-                    tma_load_4d(base + SC_B + p * SC_PANEL, &tmB, fcb, 64 * p, t, g * ca.bh,
-                                (int)b * ca.bb);
-                    if (OUT)
-                        tma_load_4d(base + SC_C + p * SC_PANEL, &tmC, fcb, 64 * p, t, g * ca.ch,
-                                    (int)b * ca.cb);
-                }
-            }
-            __syncwarp();
-            loaded_cb = c + 1;
-            if (c >= 2 && !wait2(SB_XFREE, c - 2)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(fx, SC_PANEL);
-                tma_load_4d(base + SC_X, &tmX, fx, v0, t, h * ca.xh, (int)b * ca.xb);
-            }
-            __syncwarp();
-        }
-        // a wait ran out: loads in flight may not outlive the CTA
-        if (c < nc) {
-#pragma unroll 1
-            for (int k = max(0, loaded_cb - 2); k < loaded_cb; ++k)
-                mbar_drain(bar(SB_CB + (k & 1)), (uint32_t)((k >> 1) & 1));
-#pragma unroll 1
-            for (int k = max(0, c - 2); k < c; ++k)
-                mbar_drain(bar(SB_X + (k & 1)), (uint32_t)((k >> 1) & 1));
-        }
-    } else if (warp >= 28) {
+    if (warp >= 28) {
         // ------------------------------------------------------------------ per-token factors
         // (warp 28 + k those of chunks k, k + 4, ..: one warp alone took 6,000 cycles a chunk,
         // twice what the products need)
@@ -450,14 +410,65 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                             d.z * ex2(rx + l3), d.w * ex2(rx));
             *reinterpret_cast<float4*>(&pr->eg[4 * lane]) =
                 make_float4(ex2(gp.x), ex2(gp.y), ex2(gp.z), ex2(gp.w));
-            if (lane == 0) pr->gamma = ex2(total);
+            if (lane == 0) pr->gamma = decay_f32(total * 0.6931471805599453f);
             logsum += total;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SB_PAR + c % SC_NPAR));
         }
         // the warps' sums, in a fixed order, at the end of the kernel
         if (!OUT && lane == 0) sums[warp - 28] = logsum;
-    } else if (warp >= 25 && warp < 28) {
+    } else if (warp >= 24) {
+      // (registers are released by all four warps of a group, by the same instruction, and the
+      // compiler holds what follows it to the rest: so one branch for the group)
+      regs_down<SC_REG_ISSUE>();
+      if (warp == 24) {
+        // ------------------------------------------------------------------ tiles
+        const int np = a.N > 64 ? 2 : 1;
+        int c = 0, loaded_cb = 0;
+        for (; c < nc; ++c) {
+            const uint32_t fx = bar(SB_X + (c & 1)), fcb = bar(SB_CB + (c & 1));
+            const uint32_t base = smem_u32(stage(c & 1));
+            const int t = t0 + c * SCK, ta = t + SC_AHEAD * SCK;
+            if (lane == 0 && c + SC_AHEAD < nc) {
+                tma_prefetch_4d(&tmX, v0, ta, h * ca.xh, (int)b * ca.xb);
+#pragma unroll 1
+                for (int p = 0; p < np; ++p) {
+                    tma_prefetch_4d(&tmB, 64 * p, ta, g * ca.bh, (int)b * ca.bb);
+                    if (OUT) tma_prefetch_4d(&tmC, 64 * p, ta, g * ca.ch, (int)b * ca.cb);
+                }
+            }
+            __syncwarp();
+            if (c >= 2 && !wait2(SB_CBFREE, c - 2)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(fcb, (uint32_t)(OUT ? 2 * np : np) * SC_PANEL);
+#pragma unroll 1
+                for (int p = 0; p < np; ++p) {
+                    tma_load_4d(base + SC_B + p * SC_PANEL, &tmB, fcb, 64 * p, t, g * ca.bh,
+                                (int)b * ca.bb);
+                    if (OUT)
+                        tma_load_4d(base + SC_C + p * SC_PANEL, &tmC, fcb, 64 * p, t, g * ca.ch,
+                                    (int)b * ca.cb);
+                }
+            }
+            __syncwarp();
+            loaded_cb = c + 1;
+            if (c >= 2 && !wait2(SB_XFREE, c - 2)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(fx, SC_PANEL);
+                tma_load_4d(base + SC_X, &tmX, fx, v0, t, h * ca.xh, (int)b * ca.xb);
+            }
+            __syncwarp();
+        }
+        // a wait ran out: loads in flight may not outlive the CTA
+        if (c < nc) {
+#pragma unroll 1
+            for (int k = max(0, loaded_cb - 2); k < loaded_cb; ++k)
+                mbar_drain(bar(SB_CB + (k & 1)), (uint32_t)((k >> 1) & 1));
+#pragma unroll 1
+            for (int k = max(0, c - 2); k < c; ++k)
+                mbar_drain(bar(SB_X + (k & 1)), (uint32_t)((k >> 1) & 1));
+        }
+      } else {
         // ------------------------------------------------------------------ MMAs
         // (whole warps, converged: see mma_ss. Three of them, so that no product waits for what
         // another waits for; each K step in a loop, whose few instructions stay in the first
@@ -470,6 +481,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             for (; OUT && c < n; ++c) {
                 if (!wait2(SB_CB, c)) break;
                 if (c >= 2 && !wait2(SB_Y, c - 2)) break;
+                tc_fence_after();
                 const uint32_t st = base + (c & 1) * SC_STAGE;
                 mma_kmajor(tmem + TC_SCORE + 128 * (c & 1), st + SC_C,
                            smem_desc_sw128(st + SC_B, 16, 1024), 2, SC_PANEL >> 4, a.N,
@@ -479,22 +491,35 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             }
         } else if (warp == 25) {
             // the state's
+            uint32_t slot = 0, turn = 0;  // of the scaled x
             for (; c < n; ++c) {
                 if (!wait2(SB_CB, c)) break;
-                if (!wait2(SB_XS, c)) break;
                 if (c > 0 && !wait1(SB_DSFREE, c - 1)) break;
                 tc_fence_after();
                 uint64_t da = smem_desc_sw128(base + (c & 1) * SC_STAGE + SC_B, SC_PANEL, 1024);
-                uint64_t db = smem_desc_sw128(base + SC_XS, SC_PANEL, 1024);
+                bool ok = true;
 #pragma unroll 1
-                for (uint32_t kk = 0; kk < 8; ++kk, da += 128, db += 128)
-                    mma_ss(tmem + TC_DS, da, db, idesc_bf16(128, 128, 1, 1), kk);
+                for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
+                    if (!(ok = mbar_wait_warp(bar(SB_XS + slot), turn))) break;
+                    uint64_t db =
+                        smem_desc_sw128(base + SC_XS + slot * 3 * SC_XPART, SC_XPART, 1024);
+#pragma unroll 1
+                    for (uint32_t kk = 0; kk < 2; ++kk, da += 128, db += 128) {
+                        // (one shape: only then does an accumulator's order hold)
+                        constexpr uint32_t id = idesc_bf16(128, 64, 1, 1);
+                        mma_ss(tmem + TC_DS, da, db, id, q | kk);
+                        mma_ss(tmem + TC_DS + SCV, da, db + (SC_XPART >> 4), id, q | kk);
+                        mma_ss(tmem + TC_DS + SCV, da, db + (2 * SC_XPART >> 4), id, 1);
+                    }
+                    commit_elected(bar(SB_XSFREE + q));
+                    if (++slot == SC_NXS) slot = 0, turn ^= 1;
+                }
+                if (!ok) break;
                 commit_elected(bar(SB_DS));
                 commit_elected(bar(SB_CBFREE + (c & 1)));
             }
         } else {
-            // the outputs'. (Scaled x is waited for as its writers clear the rows of x behind a
-            // sequence.)
+            // the outputs'
             for (; OUT && c < n; ++c) {
                 const uint32_t s = c & 1, st = base + s * SC_STAGE;
                 if (!wait1(SB_ST, c)) break;
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                            smem_desc_sw128(base + SC_S, SC_PANEL, 1024), 128, 4 * 128, a.N,
                            idesc_bf16(128, 64, 0, 1));
                 commit_elected(bar(SB_CBFREE + s));
-                if (!wait2(SB_XS, c)) break;
+                if (!wait2(SB_CLEAR, c)) break;
                 if (!wait2(SB_P, c)) break;
                 tc_fence_after();
                 uint64_t dx = smem_desc_sw128(st + SC_X, SC_PANEL, 1024);
@@ -522,6 +547,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             commit_elected(b0);
             mbar_drain(b0, 0);
         }
+      }
     } else if (warp < 8) {
         // ------------------------------------------------------------------ P from the scores
         // (two warps per 32 rows: the one weighs columns 0-63, the other 64-127. The P of 16 columns
@@ -595,68 +621,82 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 release_par(c);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------------------------------ scaled x
-        regs_up<SC_REG_X>();
-        const int j = tid & 127;
+        // (a thread per token and 32 channels: warps 8 + q and 12 + q the tokens 32 q ..; each 32
+        // tokens have a slot of their own, which the product frees)
+        regs_down<SC_REG_X>();
+        const int q = warp & 3, j = 32 * q + lane, half = (warp >> 2) & 1;
+        // 16-byte pieces keep their swizzled places; each lane starts at another one, so that eight
+        // lanes cover all banks
+        const int at0 = 64 * half, swz = (j & 7) << 4;
         for (int c = 0; c < nc; ++c) {
             const int s = c & 1;
             if (!wait_par(c)) break;
             const float w = par(c % SC_NPAR)->w[j];
             release_par(c);
             if (!wait2(SB_X, c)) break;
-            // rows behind a sequence are cleared in the tile of B too, once it is there
-            if (valid(c) < SCK && !wait2(SB_CB, c)) break;
             uint8_t* xr = stage(s) + SC_X + j * 128;
-            uint8_t* br = stage(s) + SC_B + j * 128;
-            uint8_t* hi = sm + SC_XS + j * 128;
             const bool live = j < valid(c);
-            // 16-byte pieces keep their swizzled places; each lane starts at another one, so that
-            // eight lanes cover all banks
-            const int turn = (j & 7) << 4;
-            uint32_t top[32], rest[32];
+            uint32_t x[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(xr + ((k << 4) ^ turn));
-                const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+            for (int k = 0; k < 4; ++k) {
+                const uint4 v = *reinterpret_cast<const uint4*>(xr + ((at0 + 16 * k) ^ swz));
+                x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+            }
+            if (valid(c) < SCK) {  // nothing behind the sequence may enter a product, not even as
+                                   // 0 * NaN: it goes from the tiles of x and (once there) of B
+                if (!wait2(SB_CB, c)) break;
+                if (!live) {
+                    uint8_t* br = stage(s) + SC_B + j * 128;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = (at0 + 16 * k) ^ swz;
+                        const uint4 z = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(xr + at) = z;
+                        *reinterpret_cast<uint4*>(br + at) = z;
+                        *reinterpret_cast<uint4*>(br + SC_PANEL + at) = z;
+                    }
+                }
+                fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(SB_CLEAR + s));
+                if (!OUT) mbar_arrive(bar(SB_XFREE + s));
+            }
+            // the slot's last use was three quarters ago. (Waited for by quarter, not by slot: that
+            // quarter's use of a chunk before is known to be over, since this warp's last one
+            // waited for it, so parity tells its phases apart.)
+            const uint32_t use = 4 * c + q, slot = use % SC_NXS, last = use - SC_NXS;
+            if (use >= SC_NXS &&
+                !mbar_wait_warp(bar(SB_XSFREE + (last & 3)), (last >> 2) & 1))
+                break;
+            uint8_t* to = sm + SC_XS + slot * 3 * SC_XPART + lane * 128;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 x = mul2(unpack2(r[e]), make_float2(w, w));
-                    top[4 * k + e] = pack2(x);
-                    rest[4 * k + e] =
-                        pack2(fma2(unpack2(top[4 * k + e]), make_float2(-1.f, -1.f), x));
+                    float2 v = mul2(unpack2(x[4 * k + e]), make_float2(w, w));
+                    p1[e] = pack2(v);
+                    v = fma2(unpack2(p1[e]), make_float2(-1.f, -1.f), v);
+                    p2[e] = pack2(v);
+                    v = fma2(unpack2(p2[e]), make_float2(-1.f, -1.f), v);
+                    p3[e] = pack2(v);
                 }
-            }
-            if (valid(c) < SCK) {  // nothing behind the sequence may enter a product
-#pragma unroll
-                for (int e = 0; e < 32; ++e) top[e] = live ? top[e] : 0u, rest[e] = live ? rest[e] : 0u;
-            }
-            if (c > 0 && !wait1(SB_DS, c - 1)) break;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                uint8_t* at = hi + ((k << 4) ^ turn);
-                *reinterpret_cast<uint4*>(at) =
-                    make_uint4(top[4 * k], top[4 * k + 1], top[4 * k + 2], top[4 * k + 3]);
-                *reinterpret_cast<uint4*>(at + SC_PANEL) =
-                    make_uint4(rest[4 * k], rest[4 * k + 1], rest[4 * k + 2], rest[4 * k + 3]);
-            }
-            if (!live) {  // .. not even as 0 * NaN
-                const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-                for (int k = 0; k < 128; k += 16) {
-                    *reinterpret_cast<uint4*>(xr + k) = z;
-                    *reinterpret_cast<uint4*>(br + k) = z;
-                    *reinterpret_cast<uint4*>(br + SC_PANEL + k) = z;
-                }
+                uint8_t* at = to + ((at0 + 16 * k) ^ swz);
+                *reinterpret_cast<uint4*>(at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+                *reinterpret_cast<uint4*>(at + SC_XPART) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                *reinterpret_cast<uint4*>(at + 2 * SC_XPART) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
             }
             fence_async_smem();
-            mbar_arrive(bar(SB_XS + s));
-            if (!OUT) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(SB_XFREE + s));
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(SB_XS + slot));
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // ------------------------------------------------------------------ the state
         regs_up<SC_REG_STATE>();
         const int n = tid & 127;
@@ -724,13 +764,12 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
         }
     } else if (warp < 24) {
         // ------------------------------------------------------------------ outputs
-        // (a thread per token and 32 channels)
-        regs_down<SC_REG_OUT>();
+        regs_up<SC_REG_OUT>();
         if constexpr (OUT) {
-            const int i = tid & 127, p0 = 32 * ((warp >> 2) & 1);
+            const int i = tid & 127;
             const float Dh = a.D ? a.D[h] : 0.f;
             __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + b * a.osb + h * a.osh +
-                                ((long)t0 + i) * a.ost + v0 + p0;
+                                ((long)t0 + i) * a.ost + v0;
             for (int c = 0; c < nc; ++c, op += SCK * a.ost) {
                 if (!wait_par(c)) break;
                 const float eg = par(c % SC_NPAR)->eg[i];
@@ -739,11 +778,11 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 // x into registers and its tile free before the products are there; outputs take
                 // its place and leave once the products' columns are free
                 const uint8_t* xr = stage(c & 1) + SC_X + i * 128;
-                uint32_t y[16];
+                uint32_t y[32];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     const uint4 v =
-                        *reinterpret_cast<const uint4*>(xr + ((2 * p0 + 16 * k) ^ ((i & 7) << 4)));
+                        *reinterpret_cast<const uint4*>(xr + ((16 * k) ^ ((i & 7) << 4)));
                     y[4 * k] = v.x, y[4 * k + 1] = v.y, y[4 * k + 2] = v.z, y[4 * k + 3] = v.w;
                 }
                 __syncwarp();
@@ -751,10 +790,10 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 if (!wait2(SB_Y, c)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
+                for (int k = 0; k < SCV; k += 8) {
                     float2 in[4], it[4];
-                    tmem_ld8(trow + TC_INTRA + p0 + k, reinterpret_cast<float*>(in));
-                    tmem_ld8(trow + TC_INTER + p0 + k, reinterpret_cast<float*>(it));
+                    tmem_ld8(trow + TC_INTRA + k, reinterpret_cast<float*>(in));
+                    tmem_ld8(trow + TC_INTER + k, reinterpret_cast<float*>(it));
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -763,17 +802,21 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 }
                 tc_fence_before();
                 mbar_arrive(bar(SB_YFREE));
-                if (i < valid(c) && p0 < pv) {
+                if (i < valid(c)) {
                     // (a store costs a cycle per row, whatever its width)
-                    if (ca.out32) {
-                        st_global_32(op, y);
-                        st_global_32(op + 16, y + 8);
-                    } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            reinterpret_cast<uint4*>(op)[k] =
-                                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-                    }
+                    for (int k = 0; k < SCV; k += 16)
+                        if (k < 32 || pv == SCV) {
+                            const uint32_t* u = y + k / 2;
+                            if (ca.out32) {
+                                st_global_32(op + k, u);
+                            } else {
+                                reinterpret_cast<uint4*>(op + k)[0] =
+                                    make_uint4(u[0], u[1], u[2], u[3]);
+                                reinterpret_cast<uint4*>(op + k)[1] =
+                                    make_uint4(u[4], u[5], u[6], u[7]);
+                            }
+                        }
                 }
             }
         }

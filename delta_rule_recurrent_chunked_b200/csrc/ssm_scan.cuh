@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
         if (tid < n) {
             const float d = ssm_delta(a, h, ssm_dt(a, b, h, tt + tid));
             sdelta[tid] = d;
-            sa[tid] = expf(d * Ah);
+            sa[tid] = decay_f32(d * Ah);
             logsum += d * Ah;
         }
         __syncthreads();
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) ssm_chain_kernel(float* state, const floa
     float4 run = *reinterpret_cast<const float4*>(p);
 #pragma unroll 4
     for (int s = 1; s < nst; ++s) {
-        const float a = expf(lg[s]);
+        const float a = decay_f32(lg[s]);
         float4 v = *reinterpret_cast<const float4*>(p + s * PN);
         run.x = fmaf(a, run.x, v.x), run.y = fmaf(a, run.y, v.y);
         run.z = fmaf(a, run.z, v.z), run.w = fmaf(a, run.w, v.w);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(32 * SSM_STEP_WARPS) ssm_step_kernel(
 #pragma unroll
     for (int u = 0; u < SSM_STEP_U; ++u) x[u] = to_f32<T>(xp[u * RPA]);
     const float delta = ssm_delta(a, h, ssm_dt(a, b, h, 0));
-    const float at = expf(delta * a.A[h]), Dh = a.D ? a.D[h] : 0.f;
+    const float at = decay_f32(delta * a.A[h]), Dh = a.D ? a.D[h] : 0.f;
     T* op = static_cast<T*>(a.out) + b * a.osb + h * a.osh + p0 + sub;
 #pragma unroll
     for (int u = 0; u < SSM_STEP_U; ++u) {

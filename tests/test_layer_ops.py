@@ -21,6 +21,14 @@ TYPES = [torch.bfloat16, torch.float32]
 EPS = 1e-6
 
 
+@pytest.fixture(autouse=True)
+def device_status_stays_clear(request):
+    """No kernel latched a status (a wait that ran out) during a GPU test."""
+    yield
+    if "gpu" in request.keywords:
+        assert drs.poll_error() == drs.DR_OK
+
+
 def rnd(gen, *shape, std=1.0, dtype=torch.float32):
     return (torch.randn(*shape, generator=gen) * std).to(dtype).cuda()
 
@@ -322,8 +330,8 @@ def ssm_inputs(seed, B, H, G, T, P, N, dtype, rows="head", state=True, ragged=Fa
 def ssm_check(i, got, dtype, T, N, what=""):
     """y: the chunked kernel rounds the weights of a chunk's tokens and the state to bf16 (2^-8
     of each product, so of mag) for bf16 inputs; in fp32 T steps of 16 u (exp of the decay, its
-    argument, two products) and a sum of N. S: fp32 sums, and for bf16 inputs delta x in two
-    bf16 halves, 2^-16 of mag."""
+    argument, two products) and a sum of N. S: fp32 sums (delta x goes in three bf16 parts, 24
+    bits)."""
     y, S, my, mS = ref.ssm(i["x"], i["dt"], i["A"], i["B"], i["C"], i["D"], i["dt_bias"], True,
                            i["S0"], i["lengths"])
     f32 = (16 * T + N + 64) * U
@@ -331,9 +339,10 @@ def ssm_check(i, got, dtype, T, N, what=""):
     within(got[0], y, H_OF[dtype] * y.abs() + ((2.0 ** -8 if bf else 0) + f32) * my, what + " y")
     assert (ref.f64(got[0])[torch.isnan(y)] == 5.0).all(), "rows behind a sequence"
     if got[1] is not None:
-        within(got[1], S, ((2.0 ** -16 if bf else 0) + f32) * mS, what + " S")
-        # over all elements the roundings average out: far below the worst case of each
-        assert float((ref.f64(got[1]) - S).norm()) <= 1e-5 * float(S.norm()) + 1e-30
+        within(got[1], S, f32 * mS, what + " S")
+        # over all elements the roundings average out, far below the worst case of each: some tens
+        # of u where the sums are not much larger than their results
+        assert float((ref.f64(got[1]) - S).norm()) <= 2e-6 * float(S.norm()) + 1e-30
 
 
 @pytest.mark.gpu
@@ -651,6 +660,29 @@ def test_short_conv_feeds_the_delta_rule_scan(oracle):
 
 
 # ------------------------------------------------------------------ streams, graphs, sizes
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,T,P,N,ragged,runs", [(8, 16, 1024, 128, 128, False, 30),
+                                                   (1, 16, 16384, 64, 128, False, 30),
+                                                   (2, 4, 4096, 64, 64, False, 60),
+                                                   (4, 16, 700, 64, 64, True, 100),
+                                                   (3, 40, 2000, 32, 32, True, 60)])
+def test_ssm_scan_gives_the_same_bits_every_time(B, H, T, P, N, ragged, runs):
+    """The chunked kernel's roles hand over to one another some thirty times a chunk: one that
+    went on too early would read what is not there yet, now and then. Every run equal, bit for
+    bit, over thousands of chunks, the first against a scan without hand-overs (per token, its
+    roundings apart from the chunked kernel's: 2^-7 of the largest output, 2^-16 of the state)."""
+    i = ssm_inputs(T + N, B, H, 1, T, P, N, torch.bfloat16, "token", ragged=ragged)
+    want = drs.ssm_scan(**{**i, "out": torch.zeros_like(i["out"])}, force_sequential=True)
+    out, S = (t.clone() for t in drs.ssm_scan(**{**i, "out": torch.zeros_like(i["out"])}))
+    assert float((out.float() - want[0].float()).abs().max()) <= 2.0 ** -7 * float(want[0].float().abs().max())
+    assert float((S - want[1]).abs().max()) <= 2.0 ** -16 * float(want[1].abs().max())
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(runs):
+        a, b = drs.ssm_scan(**{**i, "out": torch.zeros_like(i["out"])})
+        bad += (a != out).any().long() + (b != S).any().long()
+    assert int(bad) == 0
+
 
 @pytest.mark.gpu
 def test_two_streams_at_once():
