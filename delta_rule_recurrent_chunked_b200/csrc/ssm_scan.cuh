@@ -194,27 +194,33 @@ __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
 }
 
 // Chains the segments' end states in place: state s becomes the true one at the end of segment
-// s. A thread per 4 state elements of a head; grid: (B * H * P * N / 4 / block).
+// s. A thread per state element, eight segments' loads in flight; grid: B * H * P * N / block.
 __global__ void __launch_bounds__(256) ssm_chain_kernel(float* state, const float* logs, long BH,
                                                         int nst, long PN) {
-    const long e = (blockIdx.x * 256l + threadIdx.x) * 4;
+    const long e = blockIdx.x * 256l + threadIdx.x;
     if (e >= BH * PN) return;
     const long bh = e / PN;
     float* p = state + bh * nst * PN + e % PN;
     const float* lg = logs + bh * nst;
-    float4 run = *reinterpret_cast<const float4*>(p);
-#pragma unroll 4
-    for (int s = 1; s < nst; ++s) {
-        const float a = decay_f32(lg[s]);
-        float4 v = *reinterpret_cast<const float4*>(p + s * PN);
-        run.x = fmaf(a, run.x, v.x), run.y = fmaf(a, run.y, v.y);
-        run.z = fmaf(a, run.z, v.z), run.w = fmaf(a, run.w, v.w);
-        *reinterpret_cast<float4*>(p + s * PN) = run;
+    float run = p[0];
+    for (int s = 1; s < nst; s += 8) {
+        float v[8], a[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            v[k] = s + k < nst ? p[(s + k) * PN] : 0.f;
+            a[k] = s + k < nst ? decay_f32(lg[s + k]) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (s + k < nst) {
+                run = fmaf(a[k], run, v[k]);
+                p[(s + k) * PN] = run;
+            }
     }
 }
 
 inline int launch_ssm_chain(const SsmArgs& a, cudaStream_t stream) {
-    const long PN = (long)a.P * a.N, n = (long)a.B * a.H * PN / 4;
+    const long PN = (long)a.P * a.N, n = (long)a.B * a.H * PN;
     ssm_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
         a.seg_state, a.seg_log, (long)a.B * a.H, a.nseg - 1, PN);
     return cudaGetLastError() == cudaSuccess ? DR_OK : DR_ERR_CUDA;
