@@ -56,7 +56,8 @@ class ConvSplit(ctypes.Structure):
 
 # Every function the C ABI exports, with its ctypes signature.
 _VP, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
-_PV, _PS, _LL = ctypes.POINTER(DrView), ctypes.POINTER(ConvSplit), ctypes.c_longlong
+_PV = _PS = _VP  # addresses of dr_view and conv_split structs
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "dr_scan_fwd": ([_VP] * 8 + [_I] * 6 + [_VP], _I),
     "dr_scan_fwd_ex": ([_VP] * 11 + [_I] * 6 + [_VP], _I),
@@ -488,55 +489,79 @@ def chunked_applies(mode, dtype_is_bf16: bool, dk: int, dv: int) -> bool:
 
 
 # ---- around a scan: short convolution, selective state space scan, norms
+#
+# These calls are made once per layer and token, where the kernel takes some microseconds: views
+# go to the library as one array of 64-bit words (the layout of dr_view and conv_split), pointers
+# as plain integers, and a tensor that is as it should be costs one comparison of each property.
+
+_fns = {}
 
 
-def _check_rows(t, name, shape, dtype, device):
-    """A tensor of `shape` with contiguous last dimension, in any layout."""
+def _call(name, device, *args):
+    """Call an entry point with the device's current stream, with that device current."""
+    import torch
+
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    # (the stream's handle without a Stream object around it, which takes 2 us to make)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    else:
+        rc = fn(*args, stream)
+    if rc != DR_OK:
+        raise DrScanError(rc, name)
+
+
+def _rows(t, name, shape, dtype, device):
+    """Pointer of a tensor of `shape` with contiguous last dimension, in any layout."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and (
+            t.stride(-1) == 1 or shape[-1] <= 1):
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must have contiguous channels")
+    raise ValueError(f"{name} must have contiguous channels")
 
 
-def _run(name, device, *args):
-    """Call an entry point with the device's current stream, with that device current."""
-    import torch
-
-    fn = getattr(lib(), name)
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream_handle(device))
-    else:
-        rc = fn(*args, _stream_handle(device))
-    if rc != DR_OK:
-        raise DrScanError(rc, name)
+def _dense(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor, or 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, shape, dtype, device)
+    return t.data_ptr()
 
 
 def _compute_dtype(t, name):
     import torch
 
-    if t.dtype not in (torch.bfloat16, torch.float32):
+    if t.dtype is torch.bfloat16:
+        mode = DR_IN_BF16
+    elif t.dtype is torch.float32:
+        mode = 0
+    else:
         raise ValueError(f"{name} must be bf16 or fp32")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return DR_IN_BF16 if t.dtype == torch.bfloat16 else 0
+    return mode
 
 
-def _check_lengths(lengths, B, device):
-    import torch
-
-    if lengths is not None:
-        _check(lengths, "lengths", (B,), torch.int32, device)
-
-
-def _conv_splits(splits, C, K):
-    splits = [(int(s[0]), int(s[1]), bool(s[2]) if len(s) > 2 else False) for s in splits]
-    if sum(h * d for h, d, _ in splits) != C:
+def _conv_splits(splits, C, outs):
+    """(heads, dim, normalised) of each split, checked."""
+    if splits is None:
+        splits = [(C // 128, 128)]
+    splits = [(s[0], s[1], bool(s[2]) if len(s) > 2 else False) for s in splits]
+    if sum(s[0] * s[1] for s in splits) != C:
         raise ValueError(f"splits must cover the {C} channels")
+    if outs is not None and len(outs) != len(splits):
+        raise ValueError(f"outs must hold {len(splits)} tensors")
     return splits
 
 
@@ -553,27 +578,22 @@ def short_conv(x, weight, bias=None, splits=None, state0=None, lengths=None, sil
     mode = _compute_dtype(x, "x")
     B, T, C = x.shape
     K = weight.shape[-1]
-    dev = x.device
-    _check_rows(x, "x", (B, T, C), x.dtype, dev)
-    _check(weight, "weight", (C, K), torch.float32, dev)
-    if bias is not None:
-        _check(bias, "bias", (C,), torch.float32, dev)
-    if state0 is not None:
-        _check(state0, "state0", (B, K - 1, C), x.dtype, dev)
-    _check_lengths(lengths, B, dev)
-    splits = _conv_splits(splits or [(C // 128, 128)], C, K)
+    dt, dev = x.dtype, x.device
+    splits = _conv_splits(splits, C, outs)
     if outs is None:
-        outs = [torch.empty((B, h, T, d), dtype=x.dtype, device=dev) for h, d, _ in splits]
-    if len(outs) != len(splits):
-        raise ValueError(f"outs must hold {len(splits)} tensors")
-    arr = (ConvSplit * len(splits))()
+        outs = [x.new_empty((B, h, T, d)) for h, d, _ in splits]
+    words = [_rows(x, "x", x.shape, dt, dev), x.stride(0), 0, x.stride(1)]
     for i, ((h, d, n), o) in enumerate(zip(splits, outs)):
-        _check_rows(o, f"outs[{i}]", (B, h, T, d), x.dtype, dev)
-        arr[i] = ConvSplit(DrView(o.data_ptr(), *o.stride()[:3]), h, d, n)
-    state = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if want_state else None
-    _run("short_conv_fwd", dev, DrView(x.data_ptr(), x.stride(0), 0, x.stride(1)), _ptr(weight),
-         _ptr(bias), _ptr(state0), _ptr(lengths), arr, len(splits), _ptr(state), float(eps), B, T,
-         C, K, mode | (CONV_SILU if silu else 0))
+        words += (_rows(o, f"outs[{i}]", (B, h, T, d), dt, dev), *o.stride()[:3], h | d << 32, n)
+    arr = (_LL * len(words))(*words)
+    at = ctypes.addressof(arr)
+    state = x.new_empty((B, K - 1, C)) if want_state else None
+    _call("short_conv_fwd", dev, at, _dense(weight, "weight", (C, K), torch.float32, dev),
+          _dense(bias, "bias", (C,), torch.float32, dev),
+          _dense(state0, "state0", (B, K - 1, C), dt, dev),
+          _dense(lengths, "lengths", (B,), torch.int32, dev), at + 32, len(splits),
+          0 if state is None else state.data_ptr(), eps, B, T, C, K,
+          mode | CONV_SILU if silu else mode)
     return list(outs), state
 
 
@@ -585,57 +605,50 @@ def short_conv_step(x, weight, bias=None, splits=None, state=None, silu=True, ep
     mode = _compute_dtype(x, "x")
     B, C = x.shape
     K = weight.shape[-1]
-    dev = x.device
-    _check_rows(x, "x", (B, C), x.dtype, dev)
-    _check(weight, "weight", (C, K), torch.float32, dev)
-    if bias is not None:
-        _check(bias, "bias", (C,), torch.float32, dev)
+    dt, dev = x.dtype, x.device
     if state is None:
         raise ValueError("short_conv_step needs the state (updated in place)")
-    _check(state, "state", (B, K - 1, C), x.dtype, dev)
-    splits = _conv_splits(splits or [(C // 128, 128)], C, K)
+    splits = _conv_splits(splits, C, outs)
     if outs is None:
-        outs = [torch.empty((B, h, d), dtype=x.dtype, device=dev) for h, d, _ in splits]
-    if len(outs) != len(splits):
-        raise ValueError(f"outs must hold {len(splits)} tensors")
-    arr = (ConvSplit * len(splits))()
+        outs = [x.new_empty((B, h, d)) for h, d, _ in splits]
+    words = [_rows(x, "x", x.shape, dt, dev), x.stride(0), 0, 0]
     for i, ((h, d, n), o) in enumerate(zip(splits, outs)):
-        _check_rows(o, f"outs[{i}]", (B, h, d), x.dtype, dev)
-        arr[i] = ConvSplit(DrView(o.data_ptr(), o.stride(0), o.stride(1), 0), h, d, n)
-    _run("short_conv_step", dev, DrView(x.data_ptr(), x.stride(0), 0, 0), _ptr(weight),
-         _ptr(bias), _ptr(state), arr, len(splits), float(eps), B, C, K,
-         mode | (CONV_SILU if silu else 0))
+        words += (_rows(o, f"outs[{i}]", (B, h, d), dt, dev), *o.stride()[:2], 0, h | d << 32, n)
+    arr = (_LL * len(words))(*words)
+    at = ctypes.addressof(arr)
+    _call("short_conv_step", dev, at, _dense(weight, "weight", (C, K), torch.float32, dev),
+          _dense(bias, "bias", (C,), torch.float32, dev),
+          _dense(state, "state", (B, K - 1, C), dt, dev), at + 32, len(splits), eps, B, C, K,
+          mode | CONV_SILU if silu else mode)
     return list(outs)
 
 
-def _ssm_common(x, dt, A, B, C, D, dt_bias, dt_softplus, rows, force_sequential=False):
-    """Checks that ssm_scan and ssm_step share; rows: the dimensions between batch and channels
-    of x ((H, T) or (H,)). Returns (mode, N, G)."""
+def _ssm_views(x, dt, B, C, out, tokens):
+    """The words of the views x, dt, B, C, out of a scan (tokens = (T,)) or a step (()), checked;
+    with the mode bits of dt's type, G and N."""
     import torch
 
-    mode = _compute_dtype(x, "x")
-    dev, H = x.device, rows[0]
+    dev, ty = x.device, x.dtype
     G, N = B.shape[1], B.shape[-1]
-    _check_rows(x, "x", x.shape, x.dtype, dev)
-    _check_rows(B, "B", (x.shape[0], G, *rows[1:], N), x.dtype, dev)
-    _check_rows(C, "C", (x.shape[0], G, *rows[1:], N), x.dtype, dev)
-    if dt.dtype not in (torch.float32, torch.bfloat16):
+    bshape = (x.shape[0], G, *tokens, N)
+    px, po = _rows(x, "x", x.shape, ty, dev), _rows(out, "out", x.shape, ty, dev)
+    pb, pc = _rows(B, "B", bshape, ty, dev), _rows(C, "C", bshape, ty, dev)
+    if dt.dtype is torch.bfloat16:
+        mode = SSM_DT_BF16
+    elif dt.dtype is torch.float32:
+        mode = 0
+    else:
         raise ValueError("dt must be bf16 or fp32")
     if dt.shape != x.shape[:-1] or dt.device != dev:
         raise ValueError(f"dt must have shape {tuple(x.shape[:-1])} on {dev}, got "
                          f"{tuple(dt.shape)} on {dt.device}")
-    _check(A, "A", (H,), torch.float32, dev)
-    if D is not None:
-        _check(D, "D", (H,), torch.float32, dev)
-    if dt_bias is not None:
-        _check(dt_bias, "dt_bias", (H,), torch.float32, dev)
-    if dt.dtype == torch.bfloat16:
-        mode |= SSM_DT_BF16
-    if dt_softplus:
-        mode |= SSM_DT_SOFTPLUS
-    if force_sequential:
-        mode |= DR_FORCE_SEQUENTIAL
-    return mode, N, G
+    if tokens:
+        arr = (_LL * 20)(px, *x.stride()[:3], dt.data_ptr(), *dt.stride(), pb, *B.stride()[:3], pc,
+                         *C.stride()[:3], po, *out.stride()[:3])
+    else:
+        arr = (_LL * 20)(px, *x.stride()[:2], 0, dt.data_ptr(), *dt.stride(), 0, pb,
+                         *B.stride()[:2], 0, pc, *C.stride()[:2], 0, po, *out.stride()[:2], 0)
+    return arr, mode, G, N
 
 
 def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, S0=None, lengths=None,
@@ -647,23 +660,23 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, S0=None, le
     behind a sequence are left as they were). Returns (out like x, S_final fp32 or None)."""
     import torch
 
+    mode = _compute_dtype(x, "x")
     nb, H, T, P = x.shape
-    dev = x.device
-    mode, N, G = _ssm_common(x, dt, A, B, C, D, dt_bias, dt_softplus, (H, T), force_sequential)
-    if S0 is not None:
-        _check(S0, "S0", (nb, H, P, N), torch.float32, dev)
-    _check_lengths(lengths, nb, dev)
+    dev, f32 = x.device, torch.float32
     if out is None:
-        out = torch.empty((nb, H, T, P), dtype=x.dtype, device=dev)
-    _check_rows(out, "out", (nb, H, T, P), x.dtype, dev)
+        out = x.new_empty((nb, H, T, P))
+    arr, bits, G, N = _ssm_views(x, dt, B, C, out, (T,))
+    mode |= bits | (SSM_DT_SOFTPLUS if dt_softplus else 0)
+    if force_sequential:
+        mode |= DR_FORCE_SEQUENTIAL
     if want_state and S_final is None:
-        S_final = torch.empty((nb, H, P, N), dtype=torch.float32, device=dev)
-    if S_final is not None:
-        _check(S_final, "S_final", (nb, H, P, N), torch.float32, dev)
-    _run("ssm_scan_fwd", dev, DrView(x.data_ptr(), *x.stride()[:3]),
-         DrView(dt.data_ptr(), *dt.stride()), _ptr(A), DrView(B.data_ptr(), *B.stride()[:3]),
-         DrView(C.data_ptr(), *C.stride()[:3]), _ptr(D), _ptr(dt_bias), _ptr(S0), _ptr(lengths),
-         DrView(out.data_ptr(), *out.stride()[:3]), _ptr(S_final), nb, H, G, T, P, N, mode)
+        S_final = A.new_empty((nb, H, P, N))
+    at = ctypes.addressof(arr)
+    _call("ssm_scan_fwd", dev, at, at + 32, _dense(A, "A", (H,), f32, dev), at + 64, at + 96,
+          _dense(D, "D", (H,), f32, dev), _dense(dt_bias, "dt_bias", (H,), f32, dev),
+          _dense(S0, "S0", (nb, H, P, N), f32, dev),
+          _dense(lengths, "lengths", (nb,), torch.int32, dev), at + 128,
+          _dense(S_final, "S_final", (nb, H, P, N), f32, dev), nb, H, G, T, P, N, mode)
     return out, S_final
 
 
@@ -672,20 +685,19 @@ def ssm_step(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus=True, S=None, out
     B, C: [B,G,N]; S: [B,H,P,N] fp32, updated in place. Returns out [B,H,P] like x."""
     import torch
 
+    mode = _compute_dtype(x, "x")
     nb, H, P = x.shape
-    dev = x.device
-    mode, N, G = _ssm_common(x, dt, A, B, C, D, dt_bias, dt_softplus, (H,))
+    dev, f32 = x.device, torch.float32
     if S is None:
         raise ValueError("ssm_step needs the state S (updated in place)")
-    _check(S, "S", (nb, H, P, N), torch.float32, dev)
     if out is None:
-        out = torch.empty((nb, H, P), dtype=x.dtype, device=dev)
-    _check_rows(out, "out", (nb, H, P), x.dtype, dev)
-    _run("ssm_step", dev, DrView(x.data_ptr(), x.stride(0), x.stride(1), 0),
-         DrView(dt.data_ptr(), dt.stride(0), dt.stride(1), 0), _ptr(A),
-         DrView(B.data_ptr(), B.stride(0), B.stride(1), 0),
-         DrView(C.data_ptr(), C.stride(0), C.stride(1), 0), _ptr(D), _ptr(dt_bias), _ptr(S),
-         DrView(out.data_ptr(), out.stride(0), out.stride(1), 0), nb, H, G, P, N, mode)
+        out = x.new_empty((nb, H, P))
+    arr, bits, G, N = _ssm_views(x, dt, B, C, out, ())
+    at = ctypes.addressof(arr)
+    _call("ssm_step", dev, at, at + 32, _dense(A, "A", (H,), f32, dev), at + 64, at + 96,
+          _dense(D, "D", (H,), f32, dev), _dense(dt_bias, "dt_bias", (H,), f32, dev),
+          _dense(S, "S", (nb, H, P, N), f32, dev), at + 128, nb, H, G, P, N,
+          mode | bits | (SSM_DT_SOFTPLUS if dt_softplus else 0))
     return out
 
 
@@ -698,23 +710,25 @@ def gated_norm(y, gate, weight, norm_heads=1, act="silu", gate_first=False, eps=
 
     mode = _compute_dtype(y, "y")
     B, H, T, d = y.shape
-    dev = y.device
-    _check_rows(y, "y", (B, H, T, d), y.dtype, dev)
-    if gate is not None:
-        _check_rows(gate, "gate", (B, T, H * d), y.dtype, dev)
-    shared = weight.shape == (d,) and H != 1
-    _check(weight, "weight", (d,) if shared else (H * d,), torch.float32, dev)
+    dev, ty = y.device, y.dtype
+    row = (B, T, H * d)
+    shared = H != 1 and weight.shape == (d,)
     if act not in ("silu", "sigmoid"):
         raise ValueError(f'act must be "silu" or "sigmoid", got {act!r}')
     if out is None:
-        out = torch.empty((B, T, H * d), dtype=y.dtype, device=dev)
-    _check_rows(out, "out", (B, T, H * d), y.dtype, dev)
+        out = y.new_empty(row)
     mode |= ((NORM_SIGMOID if act == "sigmoid" else 0) | (NORM_GATE_FIRST if gate_first else 0)
              | (NORM_SHARED_WEIGHT if shared else 0))
-    g = None if gate is None else DrView(gate.data_ptr(), gate.stride(0), 0, gate.stride(1))
-    _run("gated_norm_fwd", dev, DrView(y.data_ptr(), *y.stride()[:3]), g, _ptr(weight),
-         DrView(out.data_ptr(), out.stride(0), 0, out.stride(1)), float(eps), B, H, T, d,
-         int(norm_heads), mode)
+    if gate is None:
+        g = (0, 0, 0, 0)
+    else:
+        g = (_rows(gate, "gate", row, ty, dev), gate.stride(0), 0, gate.stride(1))
+    arr = (_LL * 12)(_rows(y, "y", y.shape, ty, dev), *y.stride()[:3], *g,
+                     _rows(out, "out", row, ty, dev), out.stride(0), 0, out.stride(1))
+    at = ctypes.addressof(arr)
+    _call("gated_norm_fwd", dev, at, at + 32,
+          _dense(weight, "weight", (d,) if shared else (H * d,), torch.float32, dev), at + 64, eps,
+          B, H, T, d, norm_heads, mode)
     return out
 
 
@@ -728,31 +742,26 @@ def block_norm(x, weight, residual=None, scale=1.0, post_weight=None, residual_d
     import torch
 
     mode = _compute_dtype(x, "x")
-    D, dev = x.shape[-1], x.device
+    D, dev, f32 = x.shape[-1], x.device, torch.float32
     rows = x.numel() // D if D else 0
     x2 = x if x.dim() == 2 else x.view(rows, D)
-    _check_rows(x2, "x", (rows, D), x.dtype, dev)
-    _check(weight, "weight", (D,), torch.float32, dev)
-    if post_weight is not None:
-        _check(post_weight, "post_weight", (D,), torch.float32, dev)
-    scale_v = scale if torch.is_tensor(scale) else None
-    if scale_v is not None:
-        _check(scale_v, "scale", (D,), torch.float32, dev)
     rt = residual.dtype if residual is not None else residual_dtype or x.dtype
-    if rt not in (x.dtype, torch.float32):
+    if rt not in (x.dtype, f32):
         raise ValueError(f"residual must be {x.dtype} or fp32, got {rt}")
-    if residual is not None:
-        if residual_dtype not in (None, rt):
-            raise ValueError(f"residual is {rt}, not {residual_dtype}")
-        _check(residual, "residual", x.shape, rt, dev)
+    if residual is not None and residual_dtype not in (None, rt):
+        raise ValueError(f"residual is {rt}, not {residual_dtype}")
+    scale_v = 0
+    if isinstance(scale, torch.Tensor):
+        scale, scale_v = 1.0, _dense(scale, "scale", (D,), f32, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _check(out, "out", x.shape, x.dtype, dev)
+        out = x.new_empty(x.shape)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rt, device=dev)
-    _check(residual_out, "residual_out", x.shape, rt, dev)
-    _run("block_norm_fwd", dev, _ptr(x2), x2.stride(0), _ptr(residual), _ptr(weight),
-         _ptr(post_weight), _ptr(scale_v), 1.0 if scale_v is not None else float(scale),
-         _ptr(out), _ptr(residual_out), float(eps), rows, D,
-         mode | (NORM_RESIDUAL_F32 if mode and rt == torch.float32 else 0))
+        residual_out = (x if rt is x.dtype else weight).new_empty(x.shape)
+    if mode and rt is f32:
+        mode |= NORM_RESIDUAL_F32
+    _call("block_norm_fwd", dev, _rows(x2, "x", x2.shape, x.dtype, dev), x2.stride(0),
+          _dense(residual, "residual", x.shape, rt, dev), _dense(weight, "weight", (D,), f32, dev),
+          _dense(post_weight, "post_weight", (D,), f32, dev), scale_v, scale,
+          _dense(out, "out", x.shape, x.dtype, dev),
+          _dense(residual_out, "residual_out", x.shape, rt, dev), eps, rows, D, mode)
     return out, residual_out

@@ -6,6 +6,35 @@
 
 namespace drscan {
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return r;
+}
+// The two bf16 of a word, and back.
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) { return pack_bf16(x.x, x.y); }
+
 // VEC values of a tensor's type in one 16-byte access, unpacked to fp32.
 template <typename T>
 struct Vec16;
@@ -41,10 +70,24 @@ struct Vec16<__nv_bfloat16> {
     }
 };
 
-// 1 / (1 + e^-x): e^-x overflows to infinity for x < -88, where the quotient is 0 (so x times
-// it is -0, the limit). __fdividef would return 0 for denominators above 2^126 only, which is
-// the same limit.
-__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 2^x and 1 / x, approximate (2 ulp, 1 ulp), denormals as zeros.
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / (1 + e^-x), of two values. e^-x overflows to infinity for x < -88, where the quotient is 0.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+    const float2 z = mul2(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 d = add2(make_float2(ex2(z.x), ex2(z.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
 
 // log(1 + e^x) without overflow: max(x, 0) + log1p(e^-|x|).
 __device__ __forceinline__ float softplus_f32(float x) {

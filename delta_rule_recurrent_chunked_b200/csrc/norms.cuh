@@ -42,6 +42,20 @@ __device__ __forceinline__ float row_sum(float v, float* smem) {
     return v;
 }
 
+// Division of 31-bit numbers by one known at launch: multiply by the upper bits of its reciprocal
+// (Granlund and Montgomery 1994).
+struct DivBy {
+    unsigned d, mul, shift;
+    DivBy() = default;
+    explicit DivBy(unsigned d_) : d(d_), mul(0), shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned operator()(unsigned n) const {
+        return (__umulhi(n, mul) + n) >> shift;
+    }
+};
+
 struct GatedNormArgs {
     const void* y;
     long ysb, ysh, yst;
@@ -50,7 +64,8 @@ struct GatedNormArgs {
     const float* weight;
     void* out;
     long osb, ost;
-    float eps;
+    float eps, inv_w;   // 1 / (heads d)
+    DivBy by_groups, by_T;
     int B, H, T, d;
     int heads;          // of a group
     int shared_weight;  // weight has d values, the same for every head (else H d)
@@ -58,70 +73,88 @@ struct GatedNormArgs {
     int gate_first;
 };
 
-// block: NORM_BLOCK threads (TPG <= 32) or TPG; grid: rows * groups over the block's groups.
-template <typename T, int TPG, int VPT>
+// block: NORM_BLOCK threads (TPG <= 32) or TPG; grid: rows * groups over the block's groups, R
+// items each (all their loads before the first use: one 16-byte vector of y and of the gate in
+// flight per thread does not cover the latency of HBM).
+template <typename T, int TPG, int VPT, int R>
 __global__ void __launch_bounds__(TPG <= 32 ? NORM_BLOCK : TPG) gated_norm_kernel(
     const __grid_constant__ GatedNormArgs a) {
     constexpr int VEC = Vec16<T>::N;
     constexpr int GPB = TPG <= 32 ? NORM_BLOCK / TPG : 1;
     __shared__ float smem[32];
-    const int ngr = a.H / a.heads;
-    const long total = (long)a.B * a.T * ngr;
-    const long item = (long)blockIdx.x * GPB + threadIdx.x / TPG;
-    const bool live = item < total;
-    const long it = live ? item : total - 1;  // an idle group repeats the last, storing nothing
-    const int g = (int)(it % ngr);
-    const long bt = it / ngr, b = bt / a.T, t = bt % a.T;
+    const unsigned ngr = a.H / a.heads;
+    const unsigned total = (unsigned)a.B * a.T * ngr;  // below 2^31, as the entry point checks
     const int W = a.heads * a.d, nv = W / VEC, lt = threadIdx.x % TPG;
-    const T* yp = static_cast<const T*>(a.y) + b * a.ysb + t * a.yst + (long)g * a.heads * a.ysh;
-    const T* gp = a.gate ? static_cast<const T*>(a.gate) + b * a.gsb + t * a.gst + (long)g * W
-                         : nullptr;
-    T* op = static_cast<T*>(a.out) + b * a.osb + t * a.ost + (long)g * W;
+    const int dshift = __ffs(a.d) - 1;  // d is a power of two
+    const T* gate = static_cast<const T*>(a.gate);
 
-    uint4 yr[VPT], gr[VPT];
+    uint4 yr[R][VPT], gr[R][VPT];
+    T* op[R];
+    unsigned gi[R];
+    bool live[R];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = lt + i * TPG;
-        yr[i] = gr[i] = make_uint4(0, 0, 0, 0);
-        if (v < nv) {
-            const int e = v * VEC, hh = e / a.d;
-            yr[i] = *reinterpret_cast<const uint4*>(yp + hh * a.ysh + (e - hh * a.d));
-            if (gp) gr[i] = *reinterpret_cast<const uint4*>(gp + e);
-        }
-    }
-    float y[VPT][VEC], act[VPT][VEC], ss = 0.f;
+    for (int r = 0; r < R; ++r) {
+        const unsigned item = (blockIdx.x * R + r) * GPB + threadIdx.x / TPG;
+        live[r] = item < total;
+        const unsigned it = live[r] ? item : total - 1;  // an idle group repeats the last item
+        const unsigned bt = a.by_groups(it), g = it - bt * ngr, ub = a.by_T(bt);
+        const long b = ub, t = bt - ub * a.T;
+        const T* yp =
+            static_cast<const T*>(a.y) + b * a.ysb + t * a.yst + (long)g * a.heads * a.ysh;
+        const T* gp = gate + b * a.gsb + t * a.gst + (long)g * W;
+        op[r] = static_cast<T*>(a.out) + b * a.osb + t * a.ost + (long)g * W;
+        gi[r] = g;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        Vec16<T>::unpack(yr[i], y[i]);
-        float gv[VEC];
-        Vec16<T>::unpack(gr[i], gv);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const float s = sigmoid_f32(gv[j]);
-            act[i][j] = !gp ? 1.f : a.sigmoid ? s : gv[j] * s;
-            if (a.gate_first) {
-                y[i][j] *= act[i][j];
-                act[i][j] = 1.f;
+        for (int i = 0; i < VPT; ++i) {
+            const int v = lt + i * TPG;
+            yr[r][i] = gr[r][i] = make_uint4(0, 0, 0, 0);
+            if (v < nv) {
+                const int e = v * VEC, hh = e >> dshift;
+                yr[r][i] = *reinterpret_cast<const uint4*>(yp + hh * a.ysh + (e & (a.d - 1)));
+                if (gate) gr[r][i] = *reinterpret_cast<const uint4*>(gp + e);
             }
-            ss = fmaf(y[i][j], y[i][j], ss);
         }
     }
-    const float rs = rsqrtf(row_sum<TPG>(ss, smem) / (float)W + a.eps);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = lt + i * TPG;
-        if (!live || v >= nv) continue;
-        const int e = v * VEC;
-        const float* wp = a.weight + (a.shared_weight ? e % a.d : g * W + e);
+    for (int r = 0; r < R; ++r) {
+        float2 y[VPT][VEC / 2], act[VPT][VEC / 2], ss = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < VEC; j += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(wp + j);
-            y[i][j] = y[i][j] * rs * w.x * act[i][j];
-            y[i][j + 1] = y[i][j + 1] * rs * w.y * act[i][j + 1];
-            y[i][j + 2] = y[i][j + 2] * rs * w.z * act[i][j + 2];
-            y[i][j + 3] = y[i][j + 3] * rs * w.w * act[i][j + 3];
+        for (int i = 0; i < VPT; ++i) {
+            Vec16<T>::unpack(yr[r][i], reinterpret_cast<float*>(y[i]));
+            if (gate) {
+                Vec16<T>::unpack(gr[r][i], reinterpret_cast<float*>(act[i]));
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    const float2 s = sigmoid2(act[i][j]);
+                    act[i][j] = a.sigmoid ? s : mul2(act[i][j], s);
+                }
+                if (a.gate_first) {
+#pragma unroll
+                    for (int j = 0; j < VEC / 2; ++j) y[i][j] = mul2(y[i][j], act[i][j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) ss = fma2(y[i][j], y[i][j], ss);
         }
-        *reinterpret_cast<uint4*>(op + e) = Vec16<T>::pack(y[i]);
+        const float rs = rsqrtf(fmaf(row_sum<TPG>(ss.x + ss.y, smem), a.inv_w, a.eps));
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = lt + i * TPG;
+            if (!live[r] || v >= nv) continue;
+            const int e = v * VEC;
+            const float* wp = a.weight + (a.shared_weight ? e & (a.d - 1) : (int)gi[r] * W + e);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; j += 2) {
+                const float4 w = *reinterpret_cast<const float4*>(wp + 2 * j);
+                y[i][j] = mul2(mul2(y[i][j], make_float2(rs, rs)), make_float2(w.x, w.y));
+                y[i][j + 1] = mul2(mul2(y[i][j + 1], make_float2(rs, rs)), make_float2(w.z, w.w));
+            }
+            if (gate && !a.gate_first) {
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) y[i][j] = mul2(y[i][j], act[i][j]);
+            }
+            *reinterpret_cast<uint4*>(op[r] + e) = Vec16<T>::pack(reinterpret_cast<float*>(y[i]));
+        }
     }
 }
 

@@ -9,7 +9,7 @@
 // Bound: HBM. Every input is read once and every output written once, at about K + 6 flops per
 // 2 bytes. A warp owns 32 vectors of 16 bytes (256 bf16 channels) of one split and walks a tile
 // of tokens; the last K - 1 rows stay in registers as the window, so a tile re-reads K - 1 rows
-// of its neighbour only. Eight rows are loaded before the first is used. A head is 4 to 32
+// of its neighbour only. The next rows are in flight while the last ones are summed. A head is 4 to 32
 // neighbouring lanes, so its norm is a few shuffles and the head-major (or token-major) rows
 // leave in 16-byte stores.
 #pragma once
@@ -20,7 +20,8 @@ namespace drscan {
 
 constexpr int CONV_MAX_SPLITS = 4;
 constexpr int CONV_WARPS = 4;
-constexpr int CONV_ROWS = 8;  // rows in flight per thread
+constexpr int CONV_ROWS = 4;   // rows in flight per thread while four more are summed
+constexpr int CONV_CTAS = 4;    // per SM, at 128 registers (unbounded: 158 registers, 3 CTAs, slower)
 
 struct ConvSplit {
     void* out;
@@ -57,51 +58,61 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
     return v;
 }
 
-// The taps of one thread's channels.
+// The taps of one thread's channels, by pairs of channels (the sums run two to an instruction).
 template <int VEC, int K>
 struct ConvTaps {
-    float w[K][VEC], b[VEC];
+    float2 w[K][VEC / 2], b[VEC / 2];
     __device__ __forceinline__ void load(const float* weight, const float* bias, int ch0) {
+        // the taps of neighbouring channels lie together: whole 16-byte pieces
+        float t[VEC * K], c[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            b[v] = bias ? bias[ch0 + v] : 0.f;
+        for (int i = 0; i < VEC * K; i += 4)
+            *reinterpret_cast<float4*>(t + i) =
+                *reinterpret_cast<const float4*>(weight + (long)ch0 * K + i);
 #pragma unroll
-            for (int j = 0; j < K; ++j) w[j][v] = weight[(ch0 + v) * K + j];
+        for (int i = 0; i < VEC; i += 4)
+            *reinterpret_cast<float4*>(c + i) =
+                bias ? *reinterpret_cast<const float4*>(bias + ch0 + i) : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < VEC / 2; ++v) {
+            b[v] = make_float2(c[2 * v], c[2 * v + 1]);
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j][v] = make_float2(t[2 * v * K + j], t[(2 * v + 1) * K + j]);
         }
     }
 };
 
 // One row: window (oldest first) and the new row x -> the activated, normalised outputs.
 template <int VEC, int K, bool SILU>
-__device__ __forceinline__ void conv_row(const ConvTaps<VEC, K>& f, float (&win)[K - 1][VEC],
-                                         const float* x, bool normalise, int lanes, float eps,
-                                         float* y) {
-    float ss = 0.f;
+__device__ __forceinline__ void conv_row(const ConvTaps<VEC, K>& f, float2 (&win)[K - 1][VEC / 2],
+                                         const float2* x, bool normalise, int lanes, float eps,
+                                         float2* y) {
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        float c = fmaf(f.w[K - 1][v], x[v], f.b[v]);
+    for (int v = 0; v < VEC / 2; ++v) {
+        float2 c = fma2(f.w[K - 1][v], x[v], f.b[v]);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) c = fmaf(f.w[j][v], win[j][v], c);
-        y[v] = SILU ? c * sigmoid_f32(c) : c;
-        ss = fmaf(y[v], y[v], ss);
+        for (int j = 0; j < K - 1; ++j) c = fma2(f.w[j][v], win[j][v], c);
+        y[v] = SILU ? mul2(c, sigmoid2(c)) : c;
+        if (normalise) ss = fma2(y[v], y[v], ss);
     }
 #pragma unroll
     for (int j = 0; j < K - 2; ++j)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) win[j][v] = win[j + 1][v];
+        for (int v = 0; v < VEC / 2; ++v) win[j][v] = win[j + 1][v];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) win[K - 2][v] = x[v];
+    for (int v = 0; v < VEC / 2; ++v) win[K - 2][v] = x[v];
     if (normalise) {
-        const float r = rsqrtf(group_sum(ss, lanes) + eps);
+        const float r = rsqrtf(group_sum(ss.x + ss.y, lanes) + eps);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) y[v] *= r;
+        for (int v = 0; v < VEC / 2; ++v) y[v] = mul2(y[v], make_float2(r, r));
     }
 }
 
 // grid: (warp columns * B, token tiles / CONV_WARPS); block: CONV_WARPS warps, one token tile
 // each.
 template <typename T, int K, bool SILU>
-__global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_kernel(
+__global__ void __launch_bounds__(32 * CONV_WARPS, CONV_CTAS) short_conv_kernel(
     const __grid_constant__ ConvArgs a) {
     constexpr int VEC = Vec16<T>::N;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -140,25 +151,41 @@ __global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_kernel(
 
     ConvTaps<VEC, K> f;
     f.load(a.weight, a.bias, ch0);
-    float win[K - 1][VEC];
+    float2 win[K - 1][VEC / 2];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) Vec16<T>::unpack(row((long)t0 + j), win[j]);
+    for (int j = 0; j < K - 1; ++j)
+        Vec16<T>::unpack(row((long)t0 + j), reinterpret_cast<float*>(win[j]));
 
     const int lanes = sp.dim / VEC;
     const int head = v / lanes, within = v % lanes;
     T* dst = static_cast<T*>(sp.out) + b * sp.sb + head * sp.sh + within * VEC;
-    for (int t = t0; t < t1; t += CONV_ROWS) {
-        uint4 raw[CONV_ROWS];
-#pragma unroll
-        for (int i = 0; i < CONV_ROWS; ++i)
-            raw[i] = *reinterpret_cast<const uint4*>(xrow + (long)min(t + i, t1 - 1) * a.xst);
+    const T* src = xrow + (long)t0 * a.xst;
+    dst += (long)t0 * sp.st;
+    const bool normalise = sp.normalise;
+    // a group's rows are loaded while the group before is summed; rows behind the last are not read
+    uint4 raw[CONV_ROWS];
+    auto fetch = [&](int n) {
 #pragma unroll
         for (int i = 0; i < CONV_ROWS; ++i) {
-            float x[VEC], y[VEC];
-            Vec16<T>::unpack(raw[i], x);
-            conv_row<VEC, K, SILU>(f, win, x, sp.normalise, lanes, a.eps, y);
-            if (live && t + i < t1)
-                *reinterpret_cast<uint4*>(dst + (long)(t + i) * sp.st) = Vec16<T>::pack(y);
+            if (i < n) raw[i] = *reinterpret_cast<const uint4*>(src);
+            src += a.xst;
+        }
+    };
+    fetch(t1 - t0);
+    for (int t = t0; t < t1; t += CONV_ROWS) {
+        const int n = t1 - t;  // rows left
+        uint4 now[CONV_ROWS];
+#pragma unroll
+        for (int i = 0; i < CONV_ROWS; ++i) now[i] = raw[i];
+        if (n > CONV_ROWS) fetch(n - CONV_ROWS);
+#pragma unroll
+        for (int i = 0; i < CONV_ROWS; ++i) {
+            float2 x[VEC / 2], y[VEC / 2];
+            Vec16<T>::unpack(now[i], reinterpret_cast<float*>(x));
+            conv_row<VEC, K, SILU>(f, win, x, normalise, lanes, a.eps, y);
+            if (live && i < n)
+                *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(reinterpret_cast<float*>(y));
+            dst += sp.st;
         }
     }
 }
@@ -186,10 +213,10 @@ __global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_step_kernel(
     const uint4 now = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + b * a.xsb + ch0);
     ConvTaps<VEC, K> f;
     f.load(a.weight, a.bias, ch0);
-    float win[K - 1][VEC], x[VEC], y[VEC];
+    float2 win[K - 1][VEC / 2], x[VEC / 2], y[VEC / 2];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) Vec16<T>::unpack(old[j], win[j]);
-    Vec16<T>::unpack(now, x);
+    for (int j = 0; j < K - 1; ++j) Vec16<T>::unpack(old[j], reinterpret_cast<float*>(win[j]));
+    Vec16<T>::unpack(now, reinterpret_cast<float*>(x));
     const int lanes = sp.dim / VEC;
     conv_row<VEC, K, SILU>(f, win, x, sp.normalise, lanes, a.eps, y);
     __syncwarp();  // idle lanes have read the last vector's state before its owner shifts it
@@ -199,7 +226,7 @@ __global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_step_kernel(
             *reinterpret_cast<uint4*>(state + (long)j * a.C) = old[j + 1];
         *reinterpret_cast<uint4*>(state + (long)(K - 2) * a.C) = now;
         T* dst = static_cast<T*>(sp.out) + b * sp.sb + (v / lanes) * sp.sh + (v % lanes) * VEC;
-        *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(y);
+        *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(reinterpret_cast<float*>(y));
     }
 }
 

@@ -7,12 +7,13 @@
 // B and C are shared by the H / G heads of a group. It is the gated scan of this library
 // without the delta rule's correction: decay, write delta x along B, read with C.
 //
-// The rows of S are independent given (a, delta, B, C). Four neighbouring lanes hold one row,
-// N / 4 elements each in registers (elements 16 i + 4 q + 0..3 of lane q, so that the four
-// lanes' 16-byte reads of B and C from shared memory are one conflict-free 64-byte access), a
-// CTA of 128 threads 32 rows. A token costs 3 N / 4 FMA-type instructions per thread and two
-// shuffles for the readout. Bound: FMA issue (3 P N per head and token), or, with few rows, the
-// latency of the chain of tokens; the entry point then cuts the tokens into segments.
+// The rows of S are independent given (a, delta, B, C). Eight neighbouring lanes hold two rows,
+// N / 8 elements of each per lane in registers (elements 32 i + 4 q + 0..3 of lane q, so that the
+// eight lanes' 16-byte reads of B and C from shared memory are one conflict-free access), a CTA
+// of 128 threads 32 rows. A token costs a thread 3 N / 8 two-element FMA-type instructions, N / 16
+// reads and three shuffles for the readout. Bound: those reads (4 cycles each per warp and SM; with
+// one row per thread they took twice the time: 301 tokens of 128-element rows 79 us), or, with few
+// rows, the latency of the chain of tokens; the entry point then cuts the tokens into segments.
 //
 // Segments (exact): the recurrence is affine in the state it enters with, S_out = (prod a) S_in
 // + S_zero. A first launch runs every segment but the last from zero (the first from S0)
@@ -62,23 +63,26 @@ __device__ __forceinline__ float ssm_delta(const SsmArgs& a, int h, float dt) {
     return a.softplus ? softplus_f32(d) : d;
 }
 
-constexpr int SSM_TILE = 32;     // tokens staged in shared memory at a time
+constexpr int SSM_TILE = 16;     // tokens staged in shared memory at a time (32: more registers in
+                                 // flight than a third CTA per SM is worth)
 constexpr int SSM_ROWS = 32;     // rows of S per CTA
 constexpr int SSM_THREADS = 128;
+constexpr int SSM_STEPS = SSM_THREADS;  // tokens whose steps and decays are made at a time, one a
+                                        // thread (a tile's alone would take as long as its scan)
 
 // grid: (B * H * (P / SSM_ROWS), segments of this pass); block: SSM_THREADS.
 template <typename T, int N, int PASS>
 __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
     const __grid_constant__ SsmArgs a) {
-    constexpr int EPT = N / 4;
+    constexpr int EPT = N / 8;
     constexpr int VEC = Vec16<T>::N;
     __shared__ __align__(16) float sB[SSM_TILE][N];
     __shared__ __align__(16) float sC[PASS == SSM_PASS_OUTPUTS ? SSM_TILE : 1][N];
     __shared__ float sx[SSM_TILE][SSM_ROWS + 1];
     __shared__ float sy[PASS == SSM_PASS_OUTPUTS ? SSM_TILE : 1][SSM_ROWS + 1];
-    __shared__ float sdelta[SSM_TILE], sa[SSM_TILE];
+    __shared__ float sdelta[SSM_STEPS], sa[SSM_STEPS];
 
-    const int tid = threadIdx.x, q = tid & 3, r = tid >> 2;
+    const int tid = threadIdx.x, q = tid & 7, r = 2 * (tid >> 3);  // rows r and r + 1
     const int nrb = a.P / SSM_ROWS;
     const int rb = (int)(blockIdx.x % nrb);
     const long bh = blockIdx.x / nrb;
@@ -92,18 +96,21 @@ __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
     const int t0 = seg * a.seg_len;  // below T: the entry point rounds nseg to what T needs
     const int t1 = min(len, t0 + min(a.seg_len, a.T - t0));
 
-    float s[EPT];
+    float2 s[2][EPT / 2];
     const float* enter = nullptr;
     if (seg == 0)
         enter = a.S0 ? a.S0 + bh * PN + so : nullptr;
     else if (PASS == SSM_PASS_OUTPUTS)
         enter = a.seg_state + (bh * (a.nseg - 1) + seg - 1) * PN + so;
 #pragma unroll
-    for (int i = 0; i < EPT; i += 4) {
-        const float4 v = enter ? *reinterpret_cast<const float4*>(enter + 4 * i + 4 * q)
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-        s[i] = v.x, s[i + 1] = v.y, s[i + 2] = v.z, s[i + 3] = v.w;
-    }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < EPT; i += 4) {
+            const float4 v =
+                enter ? *reinterpret_cast<const float4*>(enter + k * N + 8 * i + 4 * q)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            s[k][i / 2] = make_float2(v.x, v.y), s[k][i / 2 + 1] = make_float2(v.z, v.w);
+        }
     const float Ah = a.A[h], Dh = a.D ? a.D[h] : 0.f;
     const T* xp = static_cast<const T*>(a.x.p) + b * a.x.sb + h * a.x.sh + p0;
     const T* bp = static_cast<const T*>(a.Bm.p) + b * a.Bm.sb + g * a.Bm.sh;
@@ -111,55 +118,120 @@ __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
     T* op = static_cast<T*>(a.out) + b * a.osb + h * a.osh + p0;
     float logsum = 0.f;
 
+    // a tile's loads wait in registers while the tile before is scanned
+    constexpr int NV = (SSM_TILE * (N / VEC) + SSM_THREADS - 1) / SSM_THREADS;  // pieces of B and C
+    constexpr int NX = (SSM_TILE * (SSM_ROWS / VEC) + SSM_THREADS - 1) / SSM_THREADS;
+    uint4 nextB[NV], nextC[NV], nextx[NX];
+    auto fetch = [&](int tt) {
+        const int n = min(SSM_TILE, t1 - tt);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int e = tid + k * SSM_THREADS, t = e / (N / VEC), c = (e % (N / VEC)) * VEC;
+            if (t < n) {
+                nextB[k] = *reinterpret_cast<const uint4*>(bp + (long)(tt + t) * a.Bm.st + c);
+                if constexpr (PASS == SSM_PASS_OUTPUTS)
+                    nextC[k] = *reinterpret_cast<const uint4*>(cp + (long)(tt + t) * a.Cm.st + c);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NX; ++k) {
+            const int e = tid + k * SSM_THREADS;
+            const int t = e / (SSM_ROWS / VEC), c = (e % (SSM_ROWS / VEC)) * VEC;
+            if (t < n) nextx[k] = *reinterpret_cast<const uint4*>(xp + (long)(tt + t) * a.x.st + c);
+        }
+    };
+    if (t0 < t1) fetch(t0);
     for (int tt = t0; tt < t1; tt += SSM_TILE) {
         const int n = min(SSM_TILE, t1 - tt);
         __syncthreads();  // the previous tile's readers are done
-        for (int e = tid; e < n * (N / VEC); e += SSM_THREADS) {
-            const int t = e / (N / VEC), c = (e % (N / VEC)) * VEC;
-            Vec16<T>::unpack(*reinterpret_cast<const uint4*>(bp + (long)(tt + t) * a.Bm.st + c),
-                             &sB[t][c]);
-            if constexpr (PASS == SSM_PASS_OUTPUTS)
-                Vec16<T>::unpack(
-                    *reinterpret_cast<const uint4*>(cp + (long)(tt + t) * a.Cm.st + c), &sC[t][c]);
-        }
-        for (int e = tid; e < n * (SSM_ROWS / VEC); e += SSM_THREADS) {
-            const int t = e / (SSM_ROWS / VEC), c = (e % (SSM_ROWS / VEC)) * VEC;
-            float v[VEC];
-            Vec16<T>::unpack(*reinterpret_cast<const uint4*>(xp + (long)(tt + t) * a.x.st + c), v);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) sx[t][c + i] = v[i];
+        for (int k = 0; k < NV; ++k) {
+            const int e = tid + k * SSM_THREADS, t = e / (N / VEC), c = (e % (N / VEC)) * VEC;
+            if (t < n) {
+                Vec16<T>::unpack(nextB[k], &sB[t][c]);
+                if constexpr (PASS == SSM_PASS_OUTPUTS) Vec16<T>::unpack(nextC[k], &sC[t][c]);
+            }
         }
-        if (tid < n) {
+#pragma unroll
+        for (int k = 0; k < NX; ++k) {
+            const int e = tid + k * SSM_THREADS;
+            const int t = e / (SSM_ROWS / VEC), c = (e % (SSM_ROWS / VEC)) * VEC;
+            if (t < n) {
+                float v[VEC];
+                Vec16<T>::unpack(nextx[k], v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sx[t][c + i] = v[i];
+            }
+        }
+        const int step0 = (tt - t0) & (SSM_STEPS - 1);
+        if (step0 == 0 && tt + tid < t1) {
             const float d = ssm_delta(a, h, ssm_dt(a, b, h, tt + tid));
             sdelta[tid] = d;
             sa[tid] = decay_f32(d * Ah);
             logsum += d * Ah;
         }
+        if (tt + SSM_TILE < t1) fetch(tt + SSM_TILE);
         __syncthreads();
-#pragma unroll 4
-        for (int t = 0; t < n; ++t) {
-            const float at = sa[t], u = sdelta[t] * sx[t][r];
-            float y = 0.f;
+        // one token: the rows' new states, and this lane's part of their readouts
+        auto token = [&](int t, float2* y) {
+            const float at = sa[step0 + t], d = sdelta[step0 + t];
+            const float2 a2 = make_float2(at, at);
+            const float u[2] = {d * sx[t][r], d * sx[t][r + 1]};
+            y[0] = y[1] = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < EPT; i += 4) {
-                const float4 bv = *reinterpret_cast<const float4*>(&sB[t][4 * i + 4 * q]);
-                s[i] = fmaf(at, s[i], u * bv.x);
-                s[i + 1] = fmaf(at, s[i + 1], u * bv.y);
-                s[i + 2] = fmaf(at, s[i + 2], u * bv.z);
-                s[i + 3] = fmaf(at, s[i + 3], u * bv.w);
-                if constexpr (PASS == SSM_PASS_OUTPUTS) {
-                    const float4 cv = *reinterpret_cast<const float4*>(&sC[t][4 * i + 4 * q]);
-                    y = fmaf(s[i], cv.x, y);
-                    y = fmaf(s[i + 1], cv.y, y);
-                    y = fmaf(s[i + 2], cv.z, y);
-                    y = fmaf(s[i + 3], cv.w, y);
+                const float4 bv = *reinterpret_cast<const float4*>(&sB[t][8 * i + 4 * q]);
+                float4 cv;
+                if constexpr (PASS == SSM_PASS_OUTPUTS)
+                    cv = *reinterpret_cast<const float4*>(&sC[t][8 * i + 4 * q]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 u2 = make_float2(u[k], u[k]);
+                    float2& s0 = s[k][i / 2];
+                    float2& s1 = s[k][i / 2 + 1];
+                    s0 = fma2(a2, s0, mul2(u2, make_float2(bv.x, bv.y)));
+                    s1 = fma2(a2, s1, mul2(u2, make_float2(bv.z, bv.w)));
+                    if constexpr (PASS == SSM_PASS_OUTPUTS) {
+                        y[k] = fma2(s0, make_float2(cv.x, cv.y), y[k]);
+                        y[k] = fma2(s1, make_float2(cv.z, cv.w), y[k]);
+                    }
                 }
             }
-            if constexpr (PASS == SSM_PASS_OUTPUTS) {
-                y += __shfl_xor_sync(0xffffffffu, y, 1);
-                y += __shfl_xor_sync(0xffffffffu, y, 2);
-                if (q == 0) sy[t][r] = fmaf(Dh, sx[t][r], y);
+        };
+        // the parts of M tokens added up, their shuffles side by side; lanes 0-3 go on with the
+        // first row, lanes 4-7 with the second
+        auto readout = [&](int t, const float2 (*y)[2], auto count) {
+            constexpr int M = decltype(count)::value;
+            const bool second = q & 4;
+            const int row = r + (q >> 2);
+            float v[M];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const float f0 = y[m][0].x + y[m][0].y, f1 = y[m][1].x + y[m][1].y;
+                v[m] = (second ? f1 : f0) + __shfl_xor_sync(0xffffffffu, second ? f0 : f1, 4);
             }
+#pragma unroll
+            for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], 2);
+#pragma unroll
+            for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], 1);
+            if ((q & 3) == 0) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) sy[t + m][row] = fmaf(Dh, sx[t + m][row], v[m]);
+            }
+        };
+        int t = 0;
+        for (; t + 4 <= n; t += 4) {
+            float2 y[4][2];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) token(t + m, y[m]);
+            if constexpr (PASS == SSM_PASS_OUTPUTS)
+                readout(t, y, std::integral_constant<int, 4>());
+        }
+        for (; t < n; ++t) {
+            float2 y[1][2];
+            token(t, y[0]);
+            if constexpr (PASS == SSM_PASS_OUTPUTS)
+                readout(t, y, std::integral_constant<int, 1>());
         }
         if constexpr (PASS == SSM_PASS_OUTPUTS) {
             __syncthreads();
@@ -176,20 +248,28 @@ __global__ void __launch_bounds__(SSM_THREADS) ssm_sequential_kernel(
     float* leave = nullptr;
     if (PASS == SSM_PASS_STATES) {
         leave = a.seg_state + (bh * (a.nseg - 1) + seg) * PN + so;
-        if (rb == 0 && tid < 32) {  // the tile's tokens are lanes of the first warp
+        if (rb == 0) {  // the threads' sums, in a fixed order
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1)
                 logsum += __shfl_xor_sync(0xffffffffu, logsum, off);
-            if (tid == 0) a.seg_log[bh * (a.nseg - 1) + seg] = logsum;
+            __syncthreads();
+            if ((tid & 31) == 0) sdelta[tid >> 5] = logsum;
+            __syncthreads();
+            if (tid == 0)
+                a.seg_log[bh * (a.nseg - 1) + seg] =
+                    (sdelta[0] + sdelta[1]) + (sdelta[2] + sdelta[3]);
         }
     } else if (seg == a.nseg - 1 && a.S_final) {
         leave = a.S_final + bh * PN + so;
     }
     if (leave) {
 #pragma unroll
-        for (int i = 0; i < EPT; i += 4)
-            *reinterpret_cast<float4*>(leave + 4 * i + 4 * q) =
-                make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < EPT; i += 4)
+                *reinterpret_cast<float4*>(leave + k * N + 8 * i + 4 * q) =
+                    make_float4(s[k][i / 2].x, s[k][i / 2].y, s[k][i / 2 + 1].x,
+                                s[k][i / 2 + 1].y);
     }
 }
 

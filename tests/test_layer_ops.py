@@ -65,6 +65,11 @@ def view(p=A16, sb=0, sh=0, st=0):
     return drs.DrView(p, sb, sh, st)
 
 
+def at(*views):
+    """The addresses of views (kept alive by the caller's arguments)."""
+    return [ctypes.addressof(v) for v in views]
+
+
 def call_conv(lib, x=None, w=A16, bias=None, state0=None, lengths=None, splits=None, final=None,
               eps=1e-6, B=2, T=8, C=64, K=4, mode=drs.DR_IN_BF16, step=False, state=A16):
     P = ctypes.c_void_p
@@ -73,9 +78,9 @@ def call_conv(lib, x=None, w=A16, bias=None, state0=None, lengths=None, splits=N
         splits = [drs.ConvSplit(view(sb=8 * C, sh=8 * 32, st=32), C // 32, 32, 0)]
     arr = (drs.ConvSplit * max(1, len(splits)))(*splits)
     if step:
-        return lib.short_conv_step(x, P(w), P(bias), P(state), arr, len(splits), eps, B, C, K, mode,
+        return lib.short_conv_step(*at(x), P(w), P(bias), P(state), arr, len(splits), eps, B, C, K, mode,
                                    None)
-    return lib.short_conv_fwd(x, P(w), P(bias), P(state0), P(lengths), arr, len(splits), P(final),
+    return lib.short_conv_fwd(*at(x), P(w), P(bias), P(state0), P(lengths), arr, len(splits), P(final),
                               eps, B, T, C, K, mode, None)
 
 
@@ -125,9 +130,10 @@ def call_ssm(lib, x=None, dt=None, A=A16, b=None, c=None, D=None, bias=None, S0=
     c = view(sb=G * T * N, sh=T * N, st=N) if c is None else c
     dt = view(sb=H * T, sh=T, st=1) if dt is None else dt
     if step:
-        return lib.ssm_step(x, dt, V(A), b, c, V(D), V(bias), V(S), out, B, H, G, P, N, mode, None)
-    return lib.ssm_scan_fwd(x, dt, V(A), b, c, V(D), V(bias), V(S0), V(lengths), out, V(Sf), B, H, G,
-                            T, P, N, mode, None)
+        return lib.ssm_step(*at(x, dt), V(A), *at(b, c), V(D), V(bias), V(S), *at(out), B, H, G, P, N,
+                            mode, None)
+    return lib.ssm_scan_fwd(*at(x, dt), V(A), *at(b, c), V(D), V(bias), V(S0), V(lengths), *at(out),
+                            V(Sf), B, H, G, T, P, N, mode, None)
 
 
 SSM_REFUSALS = [
@@ -165,7 +171,8 @@ def call_gated(lib, y=None, gate=None, w=A16, out=None, eps=1e-6, B=2, H=4, T=8,
     y = view(sb=H * T * d, sh=T * d, st=d) if y is None else y
     gate = view(sb=T * H * d, st=H * d) if gate is None else gate
     out = view(sb=T * H * d, st=H * d) if out is None else out
-    return lib.gated_norm_fwd(y, gate, ctypes.c_void_p(w), out, eps, B, H, T, d, heads, mode, None)
+    return lib.gated_norm_fwd(*at(y, gate), ctypes.c_void_p(w), *at(out), eps, B, H, T, d, heads,
+                              mode, None)
 
 
 @pytest.mark.parametrize("kw,code", [
