@@ -15,11 +15,9 @@ LIB = os.path.join(PKG, "libdrscan.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC",
+    "-shared", "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
-# The scans and the operators around them: two units, compiled at the same time.
-UNITS = ["drscan.cu", "layer.cu"]
 
 
 def _sources():
@@ -35,31 +33,17 @@ def needs_build() -> bool:
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile the units of csrc (which include every kernel) into libdrscan.so."""
+    """Compile csrc/library.cu (which includes every kernel) into libdrscan.so."""
     if not force and not needs_build():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
-    objects, running = [], []
-    for unit in UNITS:
-        objects.append(f"{tmp}.{unit}.o")
-        cmd = [nvcc, *NVCC_FLAGS, "-I" + INCLUDE, "-c", "-o", objects[-1],
-               os.path.join(CSRC, unit)]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-            print(" ".join(cmd), file=sys.stderr)
-        running.append((cmd, subprocess.Popen(cmd)))
-    try:
-        codes = [(cmd, p.wait()) for cmd, p in running]
-        for cmd, code in codes:
-            if code:
-                raise subprocess.CalledProcessError(code, cmd)
-        subprocess.check_call([nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objects])
-        os.replace(tmp, LIB)
-    finally:
-        for o in objects:
-            if os.path.exists(o):
-                os.remove(o)
+    cmd = [nvcc, *NVCC_FLAGS, "-I" + INCLUDE, "-o", tmp, os.path.join(CSRC, "library.cu")]
+    if verbose:
+        cmd.insert(1, "-Xptxas=-v")
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, LIB)
     return LIB
 
 

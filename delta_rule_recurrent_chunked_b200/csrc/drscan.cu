@@ -1,7 +1,7 @@
 // C-ABI entry points of libdrscan: argument validation, kernel selection and launch.
 // The declarations, with the meaning and layout of every argument, are in drscan.h.
-// The scan kernels live in this one translation unit so that they share the device status
-// word without relocatable device code; the kernels of layer.cu share that unit's own.
+// All kernels live in this one translation unit so that they share the device status
+// word without relocatable device code.
 #include <climits>
 #include <cstdint>
 #include <cstdio>
@@ -11,45 +11,25 @@
 #include "dr_chunked.cuh"
 #include "dr_decode.cuh"
 #include "dr_sequential.cuh"
-#include "entry.cuh"
 #include "loglinear.cuh"
 #include "vla_chunked.cuh"
 #include "vla_sequential.cuh"
 
 using namespace drscan;
 
-// Stream-ordered scratch from a memory pool of this library's own, one per device, that
-// keeps its memory between calls (release threshold at the maximum), so that a call after
-// the first one does not go to the driver for memory.
-int drscan::scratch_alloc(void** p, size_t bytes, cudaStream_t stream) {
-    constexpr int kMaxDev = 64;
-    static std::mutex mu;
-    static cudaMemPool_t pools[kMaxDev] = {};
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return DR_ERR_CUDA;
-    cudaMemPool_t pool;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!pools[dev]) {
-            cudaMemPoolProps props = {};
-            props.allocType = cudaMemAllocationTypePinned;
-            props.handleTypes = cudaMemHandleTypeNone;
-            props.location.type = cudaMemLocationTypeDevice;
-            props.location.id = dev;
-            cudaMemPool_t created;
-            if (cudaMemPoolCreate(&created, &props) != cudaSuccess) return DR_ERR_CUDA;
-            uint64_t keep = UINT64_MAX;
-            cudaMemPoolSetAttribute(created, cudaMemPoolAttrReleaseThreshold, &keep);
-            pools[dev] = created;
-        }
-        pool = pools[dev];
-    }
-    return cudaMallocFromPoolAsync(p, bytes, pool, stream) == cudaSuccess ? DR_OK : DR_ERR_CUDA;
-}
-
 namespace {
 
 constexpr int kVersion = 100;  // 0.1.0
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
+bool ok_opt(const void* p) { return p == nullptr || aligned16(p); }
+bool dim_supported(int d) { return d == 32 || d == 64 || d == 128; }
+
+int launch_status() {
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? DR_OK : DR_ERR_CUDA;
+}
 
 // Arguments of a decode step (device pointers as dr_decode_step_ex receives them).
 struct DecodeArgs {
@@ -142,6 +122,15 @@ int dispatch_sequential(const ChunkArgs& a, int dk, int variant, cudaStream_t st
     return DR_ERR_INVALID_ARG;
 }
 
+// State handed through unchanged when there are no tokens: S_final = S0 (or zeros).
+int copy_state(float* dst, const float* src, size_t count, cudaStream_t stream) {
+    if (!dst) return DR_OK;
+    cudaError_t e = src ? cudaMemcpyAsync(dst, src, count * sizeof(float),
+                                          cudaMemcpyDeviceToDevice, stream)
+                        : cudaMemsetAsync(dst, 0, count * sizeof(float), stream);
+    return e == cudaSuccess ? DR_OK : DR_ERR_CUDA;
+}
+
 // Gated DeltaNet-2's erase directions e = b (.) k and write targets z = w (.) v in bf16 (each
 // product in fp32, rounded to nearest even), for the chunked path, which then runs Gated
 // DeltaNet on (q, e, z). A thread per 8 consecutive elements: the k part, then the v part.
@@ -190,6 +179,35 @@ int launch_vla(const float* q, const float* k, const float* v, const float* u, c
     kern<<<(unsigned)BH, 2 * D, smem, stream>>>(q, k, v, u, S0, A0, n0, lambda0, out, S_final,
                                                 A_final, n_final, T);
     return launch_status();
+}
+
+// Stream-ordered scratch from a memory pool of this library's own, one per device, that
+// keeps its memory between calls (release threshold at the maximum), so that a call after
+// the first one does not go to the driver for memory.
+int scratch_alloc(void** p, size_t bytes, cudaStream_t stream) {
+    constexpr int kMaxDev = 64;
+    static std::mutex mu;
+    static cudaMemPool_t pools[kMaxDev] = {};
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return DR_ERR_CUDA;
+    cudaMemPool_t pool;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!pools[dev]) {
+            cudaMemPoolProps props = {};
+            props.allocType = cudaMemAllocationTypePinned;
+            props.handleTypes = cudaMemHandleTypeNone;
+            props.location.type = cudaMemLocationTypeDevice;
+            props.location.id = dev;
+            cudaMemPool_t created;
+            if (cudaMemPoolCreate(&created, &props) != cudaSuccess) return DR_ERR_CUDA;
+            uint64_t keep = UINT64_MAX;
+            cudaMemPoolSetAttribute(created, cudaMemPoolAttrReleaseThreshold, &keep);
+            pools[dev] = created;
+        }
+        pool = pools[dev];
+    }
+    return cudaMallocFromPoolAsync(p, bytes, pool, stream) == cudaSuccess ? DR_OK : DR_ERR_CUDA;
 }
 
 // The segmented scan (steps in dr_chunked.cuh) of Gated DeltaNet or KDA: scratch for two sets
@@ -711,9 +729,6 @@ int dr_poll_error(cudaStream_t stream) {
         const int zero = 0;
         if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) return DR_ERR_CUDA;
     }
-    int layer = 0;
-    if (layer_poll_status(&layer) != DR_OK) return DR_ERR_CUDA;
-    if (status == 0) status = layer;
     return status;
 }
 

@@ -1,10 +1,11 @@
 // C-ABI entry points of the operators around a scan: the short convolution, the selective
 // state space scan and its one-token step, and the norms. Argument validation, kernel selection
-// and launch; the declarations, with the meaning of every argument, are in drscan.h.
+// and launch; the declarations, with the meaning of every argument, are in drscan.h. Part of the
+// translation unit of library.cu, behind drscan.cu: it shares that file's status word, checks of
+// pointers, state copy and scratch pool.
 #include <algorithm>
 #include <climits>
 
-#include "entry.cuh"
 #include "norms.cuh"
 #include "short_conv.cuh"
 #include "ssm_chunked.cuh"
@@ -297,16 +298,6 @@ struct BlockLaunch {
 };
 
 }  // namespace
-
-// This unit's status word (see dr_poll_error), cleared when read.
-int drscan::layer_poll_status(int* status) {
-    *status = 0;
-    if (cudaMemcpyFromSymbol(status, g_status, sizeof(int)) != cudaSuccess) return DR_ERR_CUDA;
-    const int zero = 0;
-    if (*status != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess)
-        return DR_ERR_CUDA;
-    return DR_OK;
-}
 
 extern "C" {
 
