@@ -557,7 +557,7 @@ def _conv_splits(splits, C, outs):
     """(heads, dim, normalised) of each split, checked."""
     if splits is None:
         splits = [(C // 128, 128)]
-    splits = [(s[0], s[1], bool(s[2]) if len(s) > 2 else False) for s in splits]
+    splits = [(int(s[0]), int(s[1]), bool(s[2]) if len(s) > 2 else False) for s in splits]
     if sum(s[0] * s[1] for s in splits) != C:
         raise ValueError(f"splits must cover the {C} channels")
     if outs is not None and len(outs) != len(splits):

@@ -48,10 +48,11 @@ int launch_conv(const ConvArgs& a, bool step, cudaStream_t stream) {
         return launch_status();
     }
     ConvArgs c = a;
-    // Tokens per warp: as long as the launch still fills the GPU several times over, since a tile
+    // Tokens per warp: up to 64 as long as the launch still has 64 warps for each SM, since a tile
     // reads the taps and K - 1 rows of its neighbour again.
-    c.tile = CONV_ROWS;
-    while (c.tile < 64 && (long)a.ncols * a.B * ((a.T + 2 * c.tile - 1) / (2 * c.tile)) >= 148 * 64)
+    c.tile = 2 * CONV_ROWS;
+    while (c.tile < 64 &&
+           (long)a.ncols * a.B * (((long)a.T + 2 * c.tile - 1) / (2 * c.tile)) >= 148 * 64)
         c.tile *= 2;
     const long tiles = ((long)a.T + c.tile - 1) / c.tile;
     const long gy = (tiles + CONV_WARPS - 1) / CONV_WARPS, gx = (long)a.ncols * a.B;
@@ -331,7 +332,6 @@ int short_conv_step(const dr_view* x, const float* weight, const float* bias, vo
     if (rc != DR_OK) return rc;
     if (!ok_opt(state) || (B > 0 && !state)) return DR_ERR_INVALID_ARG;
     if (B == 0) return DR_OK;
-    // two sequences of one row of x would be two states of one token: allowed (stride 0)
     a.state_final = state;
     const bool silu = (mode & CONV_SILU) != 0;
     return (mode & DR_IN_BF16) ? dispatch_conv<__nv_bfloat16>(a, K, silu, true, stream)

@@ -56,7 +56,8 @@ enum {
 /* q, k, v and out are bf16 (else fp32). beta, gate, S0 and S_final are always fp32. */
 #define DR_IN_BF16 0x100
 /* Use the per-token kernel (fp32 state, CUDA cores) even where the chunked tensor-core
- * kernel applies. Same results up to rounding; slower. For testing and as a baseline. */
+ * kernel applies (ssm_scan_fwd too). Same results up to rounding; slower. For testing and as a
+ * baseline. */
 #define DR_FORCE_SEQUENTIAL 0x200
 /* Keep DeltaNet, Gated DeltaNet and KDA on the chained chunked kernel (one pass, one dependent
  * chain of chunks per head) where dr_scan_fwd would take the segmented scan (see dr_scan_fwd). */
@@ -377,9 +378,9 @@ typedef struct conv_split {
  *                together where it is shorter), or NULL to skip; not state0 itself
  *   mode         DR_IN_BF16? | CONV_SILU?
  *
- * Supported: K in {2,3,4}, dim in {32, 64, 128}; T = 0 copies state0. Sums in fp32, one
- * rounding per output. Outputs may not alias inputs. Returns DR_OK or a negative status; on
- * error nothing is launched.
+ * Supported: K in {2,3,4}, dim in {32, 64, 128}, T up to 2^21 at least (DR_ERR_UNSUPPORTED past
+ * what a grid can hold); T = 0 copies state0. Sums in fp32, one rounding per output. Outputs may
+ * not alias inputs. Returns DR_OK or a negative status; on error nothing is launched.
  */
 int short_conv_fwd(const dr_view* x, const float* weight, const float* bias, const void* state0,
                    const int* lengths, const conv_split* splits, int nsplit, void* state_final,
@@ -412,8 +413,12 @@ int short_conv_step(const dr_view* x, const float* weight, const float* bias, vo
  *            there; S_final is the state after the last token
  *   mode     DR_IN_BF16? | SSM_DT_SOFTPLUS? | SSM_DT_BF16? | DR_FORCE_SEQUENTIAL?
  *
- * Supported: P, N in {32, 64, 128}, H a multiple of G. The steps decay: delta A <= 0 (growth is
- * computed as written while exp stays finite). Sequences too few to fill the GPU are cut into
+ * Supported: P, N in {32, 64, 128}, H a multiple of G. bf16 inputs of more than 2048 / N tokens
+ * run the chunked kernel (128-token chunks on tcgen05 tensor cores; weights of a chunk's tokens and
+ * the state that the outputs read in bf16, the state itself in fp32 throughout), everything else
+ * the per-token kernel on CUDA cores. The steps decay: delta A <= 0 (growth is computed as written
+ * while exp stays finite). A NaN or infinity among a sequence's own x, Bm, Cm or dt reaches outputs
+ * of its whole 128-token chunk in the chunked kernel. Sequences too few to fill the GPU are cut into
  * segments, whose states take B*H*(segments-1)*(P*N+1) floats of scratch from the library's
  * stream-ordered pool (DR_ERR_CUDA if it cannot be had); the result is that of the uncut scan
  * up to fp32 rounding. T = 0 copies S0. out may not alias an input. Returns DR_OK or a negative
@@ -447,8 +452,9 @@ int ssm_step(const dr_view* x, const dr_view* dt, const float* A, const dr_view*
  *   out     [B,T,H d] view like y (sb, st)
  *   mode    DR_IN_BF16? | NORM_SIGMOID? | NORM_GATE_FIRST? | NORM_SHARED_WEIGHT?
  *
- * Supported: d in {32, 64, 128}, W <= 16384 (bf16) or 8192 (fp32). Statistics in fp32, one
- * rounding per output. out may not alias y; it may be gate itself, with the same strides.
+ * Supported: d in {32, 64, 128}, W <= 16384 (bf16) or 8192 (fp32), B*T*(H/norm_heads) < 2^31.
+ * Statistics in fp32, one rounding per output. out may not alias y; it may be gate itself, with
+ * the same strides.
  */
 int gated_norm_fwd(const dr_view* y, const dr_view* gate, const float* weight, const dr_view* out,
                    float eps, int B, int H, int T, int d, int norm_heads, int mode,
