@@ -5,6 +5,7 @@
 // pointers, state copy and scratch pool.
 #include <algorithm>
 #include <climits>
+#include <utility>
 
 #include "norms.cuh"
 #include "short_conv.cuh"
@@ -27,13 +28,18 @@ bool ok_view(const dr_view* v, long nb, long nh, long nt, int esize) {
     return true;
 }
 
-// The same for a view that is written: no two rows may be the same memory.
+// The same for a view that is written: no two rows may be the same memory. From the dimension of
+// the smallest stride on, each steps over all that those before it span.
 bool ok_out_view(const dr_view* v, long nb, long nh, long nt, int width, int esize) {
     if (!ok_view(v, nb, nh, nt, esize)) return false;
-    const long long s[3] = {v->sb, v->sh, v->st};
-    const long n[3] = {nb, nh, nt};
-    for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && s[i] < width) return false;
+    std::pair<long long, long> dim[3] = {{v->sb, nb}, {v->sh, nh}, {v->st, nt}};
+    std::sort(dim, dim + 3);
+    double span = width;  // exact as far as memory reaches
+    for (const auto& [stride, n] : dim) {
+        if (n <= 1) continue;
+        if ((double)stride < span) return false;
+        span += (double)stride * (double)(n - 1);
+    }
     return true;
 }
 

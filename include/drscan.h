@@ -335,8 +335,9 @@ int loglinear_scan_fwd(const void* q, const void* k, const void* v, const float*
 /* A tensor of B x H x T rows of contiguous channels, with element strides of batch, head and
  * token, so that a projection's columns, [B,H,T,d] and [B,T,H,d] are all read and written in
  * place. The data is 16-byte aligned; the strides are >= 0 and whole multiples of 16 bytes (0
- * repeats a row; not in an output, whose strides are at least a row). A stride whose dimension
- * has size one, or that the argument's description leaves out, is not used. */
+ * repeats a row; not in an output, where each dimension steps over all that the dimensions of
+ * smaller strides span, so that no two rows share memory). A stride whose dimension has size one,
+ * or that the argument's description leaves out, is not used. */
 typedef struct dr_view {
     void* data;
     long long sb, sh, st;

@@ -102,6 +102,7 @@ INV, UNS, OK = drs.DR_ERR_INVALID_ARG, drs.DR_ERR_UNSUPPORTED, drs.DR_OK
     (dict(splits=[drs.ConvSplit(view(None, 512, 256, 32), 2, 32, 0)]), INV),
     (dict(splits=[drs.ConvSplit(view(A16, 512, 256, 0), 2, 32, 0)]), INV),         # rows overlap
     (dict(splits=[drs.ConvSplit(view(A16, 512, 16, 32), 2, 32, 0)]), INV),
+    (dict(splits=[drs.ConvSplit(view(A16, 256, 256, 32), 2, 32, 0)]), INV),  # batches into heads
     (dict(splits=[drs.ConvSplit(view(sb=512, sh=256, st=32), 4, 16, 0)]), UNS),
     (dict(K=5), UNS), (dict(K=1), UNS),
     (dict(splits=[drs.ConvSplit(view(sb=512, sh=256, st=32), 1, 32, 0)] * 5, C=160,
@@ -141,6 +142,7 @@ SSM_REFUSALS = [
     (dict(x=view(None, 8, 8, 8)), INV), (dict(x=view(A16 + 8, 2048, 512, 64)), INV),
     (dict(b=view(A16, 1024, 512, 60)), INV) , (dict(c=view(A16, -8, 512, 64)), INV),
     (dict(out=view(A16, 2048, 0, 64)), INV),        # heads written over one another
+    (dict(out=view(A16, 64, 64, 2048)), INV),       # batches over heads, in a scan and in a step
     (dict(dt=view(None)), INV), (dict(dt=view(A16 + 2, 32, 8, 1)), INV),
     (dict(dt=view(A16 + 1, 32, 8, 1), mode=drs.DR_IN_BF16 | drs.SSM_DT_BF16), INV),
     (dict(G=3), INV), (dict(G=0), INV), (dict(H=-1), INV), (dict(P=0), INV),
@@ -178,6 +180,7 @@ def call_gated(lib, y=None, gate=None, w=A16, out=None, eps=1e-6, B=2, H=4, T=8,
 @pytest.mark.parametrize("kw,code", [
     (dict(w=None), INV), (dict(w=A16 + 4), INV), (dict(y=view(None)), INV),
     (dict(out=view(None)), INV), (dict(out=view(A16, 2048, 0, 64)), INV),
+    (dict(out=view(A16, 1024, 0, 256)), INV),       # the second sequence's rows among the first's
     (dict(gate=view(A16 + 2, 2048, 0, 256)), INV), (dict(heads=3), INV), (dict(heads=0), INV),
     (dict(eps=-1.0), INV), (dict(mode=0x8000), INV), (dict(d=48), UNS),
     (dict(H=512, heads=512), UNS), (dict(H=128, heads=128, d=128, mode=0), UNS),
