@@ -60,7 +60,7 @@ int launch_conv(const ConvArgs& a, bool step, cudaStream_t stream) {
     while (c.tile < 64 &&
            (long)a.ncols * a.B * (((long)a.T + 2 * c.tile - 1) / (2 * c.tile)) >= 148 * 64)
         c.tile *= 2;
-    const long tiles = ((long)a.T + c.tile - 1) / c.tile;
+    const long tiles = ((long)a.T + c.tile - 1) / c.tile;  // of 64 for all that a grid cannot hold
     const long gy = (tiles + CONV_WARPS - 1) / CONV_WARPS, gx = (long)a.ncols * a.B;
     if (gx > INT_MAX || gy > 65535) return DR_ERR_UNSUPPORTED;
     short_conv_kernel<T, K, SILU>
@@ -356,6 +356,7 @@ int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_v
     if (!ok_opt(S0) || !ok_opt(S_final) || (reinterpret_cast<uintptr_t>(lengths) & 3))
         return DR_ERR_INVALID_ARG;
     if (S0 && S0 == S_final) return DR_ERR_INVALID_ARG;
+    if (T > 1 << 30) return DR_ERR_UNSUPPORTED;  // tokens are counted in 32 bits, a chunk beyond T
     const long BH = (long)B * H;
     if (BH == 0) return DR_OK;
     const size_t PN = (size_t)P * N;

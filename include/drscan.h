@@ -379,9 +379,8 @@ typedef struct conv_split {
  *                together where it is shorter), or NULL to skip; not state0 itself
  *   mode         DR_IN_BF16? | CONV_SILU?
  *
- * Supported: K in {2,3,4}, dim in {32, 64, 128}, T up to 2^21 at least (DR_ERR_UNSUPPORTED past
- * what a grid can hold); T = 0 copies state0. Sums in fp32, one rounding per output. Outputs may
- * not alias inputs. Returns DR_OK or a negative status; on error nothing is launched.
+ * Supported: K in {2,3,4}, dim in {32, 64, 128}, T <= 16776960; T = 0 copies state0. Sums in
+ * fp32, one rounding per output. Outputs may not alias inputs. Returns DR_OK or a negative status; on error nothing is launched.
  */
 int short_conv_fwd(const dr_view* x, const float* weight, const float* bias, const void* state0,
                    const int* lengths, const conv_split* splits, int nsplit, void* state_final,
@@ -414,10 +413,10 @@ int short_conv_step(const dr_view* x, const float* weight, const float* bias, vo
  *            there; S_final is the state after the last token
  *   mode     DR_IN_BF16? | SSM_DT_SOFTPLUS? | SSM_DT_BF16? | DR_FORCE_SEQUENTIAL?
  *
- * Supported: P, N in {32, 64, 128}, H a multiple of G. bf16 inputs of more than 2048 / N tokens
- * run the chunked kernel (128-token chunks on tcgen05 tensor cores; weights of a chunk's tokens and
- * the state that the outputs read in bf16, the state itself in fp32 throughout), everything else
- * the per-token kernel on CUDA cores. The steps decay: delta A <= 0 (growth is computed as written
+ * Supported: P, N in {32, 64, 128}, H a multiple of G, T <= 2^30. bf16 inputs of more than
+ * 2048 / N tokens run the chunked kernel (128-token chunks on tcgen05 tensor cores; weights of a
+ * chunk's tokens and the state that the outputs read in bf16, the state itself in fp32
+ * throughout), everything else the per-token kernel on CUDA cores. The steps decay: delta A <= 0 (growth is computed as written
  * while exp stays finite). A NaN or infinity among a sequence's own x, Bm, Cm or dt reaches outputs
  * of its whole 128-token chunk in the chunked kernel. Sequences too few to fill the GPU are cut into
  * segments, whose states take B*H*(segments-1)*(P*N+1) floats of scratch from the library's

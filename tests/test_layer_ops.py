@@ -105,6 +105,8 @@ INV, UNS, OK = drs.DR_ERR_INVALID_ARG, drs.DR_ERR_UNSUPPORTED, drs.DR_OK
     (dict(splits=[drs.ConvSplit(view(A16, 256, 256, 32), 2, 32, 0)]), INV),  # batches into heads
     (dict(splits=[drs.ConvSplit(view(sb=512, sh=256, st=32), 4, 16, 0)]), UNS),
     (dict(K=5), UNS), (dict(K=1), UNS),
+    (dict(T=16776961, B=1, splits=[drs.ConvSplit(view(sh=1 << 30, st=32), 2, 32, 0)]), UNS),
+    (dict(T=(1 << 31) - 1, B=1, splits=[drs.ConvSplit(view(sh=1 << 36, st=32), 2, 32, 0)]), UNS),
     (dict(splits=[drs.ConvSplit(view(sb=512, sh=256, st=32), 1, 32, 0)] * 5, C=160,
           x=view(sb=2000, st=160)), UNS),
     (dict(B=0), OK), (dict(B=0, x=view(None)), OK), (dict(T=0), OK), (dict(T=0, w=None), OK),
@@ -155,6 +157,8 @@ SSM_REFUSALS = [
 @pytest.mark.parametrize("kw,code", SSM_REFUSALS + [
     (dict(S0=A16 + 8), INV), (dict(Sf=A16 + 8), INV), (dict(S0=A16, Sf=A16), INV),
     (dict(lengths=A16 + 1), INV), (dict(T=-1), INV), (dict(T=0, x=view(None)), OK),
+    (dict(T=(1 << 30) + 1), UNS), (dict(T=(1 << 31) - 1, B=1, H=1, G=1), UNS),
+    (dict(T=(1 << 31) - 1, B=1, H=1, G=1, mode=0), UNS),
 ])
 def test_ssm_scan_refusals(lib, kw, code):
     assert call_ssm(lib, **kw) == code
