@@ -351,7 +351,14 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             // four neighbouring tokens per lane: sums from the chunk's left (inclusive) and right
             // (exclusive: short near the chunk's end, where the weights of the state are largest)
             const float4 d = *reinterpret_cast<const float4*>(&pr->delta[4 * lane]);
-            const float l0 = d.x * Ah, l1 = d.y * Ah, l2 = d.z * Ah, l3 = d.w * Ah;
+            // a decay below 2^-160 is none at all in fp32; taken as 2^-160 it keeps g within 128 * 160,
+            // where differences of g are exact to 2^-9 (a token that wipes the state may decay by far
+            // more, and would drown the steps behind it)
+            const auto step = [Ah](float dt) {
+                const float l = dt * Ah;
+                return l < -160.f ? -160.f : l;
+            };
+            const float l0 = step(d.x), l1 = step(d.y), l2 = step(d.z), l3 = step(d.w);
             const float q1 = l0 + l1, q2 = q1 + l2, q3 = q2 + l3;
             float left = q3, right = q3;
 #pragma unroll

@@ -393,6 +393,20 @@ def test_ssm_scan_decays(dtype, rate):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rate", [30.0, 4e4])
+def test_ssm_scan_tokens_that_wipe_the_state(dtype, rate):
+    """Now and then a token whose decay underflows by far, among tokens that hardly decay."""
+    T = 300
+    i = ssm_inputs(5, 2, 2, 1, T, 64, 64, dtype)
+    i["dt_bias"], i["A"] = None, torch.full_like(i["A"], -rate)
+    i["dt"] = torch.full_like(i["dt"], math.log(1e-3 / rate))  # delta of 1e-3 / rate
+    for t in (5, 70, 71, 128, 200, 255):
+        i["dt"][:, :, t] = 30.0
+    ssm_check(i, drs.ssm_scan(**i), dtype, T, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES)
 def test_ssm_scan_garbage_behind_a_sequence(dtype):
     i = ssm_inputs(11, 3, 2, 1, 200, 64, 64, dtype)
     i["lengths"] = torch.tensor([77, 200, 128], dtype=torch.int32).cuda()
