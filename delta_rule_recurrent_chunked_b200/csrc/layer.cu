@@ -246,8 +246,8 @@ int ssm_args(SsmArgs* a, const dr_view* x, const dr_view* dt, const float* A, co
 // ------------------------------------------------------------------ norms
 
 // Runs `launch` with the threads per row (TPG) and vectors per thread (VPT) for rows of nv
-// 16-byte vectors: the fewest threads that leave a thread one vector (rows up to a warp), then
-// up to four (measured in norms.cuh).
+// 16-byte vectors: one vector a thread as long as a row fits a warp, whose sums need no barrier
+// then; then up to four, what a thread can have in flight.
 template <typename F>
 int with_row_shape(int nv, F&& launch) {
     if (nv <= 4) return launch.template operator()<4, 1>();

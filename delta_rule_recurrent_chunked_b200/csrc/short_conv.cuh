@@ -6,12 +6,20 @@
 //
 // x_{-1}, x_{-2}, .. come from state0, the K - 1 inputs before the sequence (zeros without it).
 //
-// Bound: HBM. Every input is read once and every output written once, at about K + 6 flops per
+// Floor: HBM. Every input is read once and every output written once, at about K + 6 flops per
 // 2 bytes. A warp owns 32 vectors of 16 bytes (256 bf16 channels) of one split and walks a tile
 // of tokens; the last K - 1 rows stay in registers as the window, so a tile re-reads K - 1 rows
 // of its neighbour only. The next rows are in flight while the last ones are summed. A head is 4 to 32
 // neighbouring lanes, so its norm is a few shuffles and the head-major (or token-major) rows
 // leave in 16-byte stores.
+//
+// Measured, q, k and v of 16 heads of 128 (6144 bf16 channels, q and k normalised) for 8 x 4096
+// tokens, 805 MB: 170 us, 4.7 TB/s, 73% of the measured copy rate. The loads and stores alone take
+// 137 us, without SiLU 158: the rest is the issue and latency of some hundred instructions per
+// 16 bytes on the 16 warps that the window and the taps leave room for (issue slots 50%, special
+// functions 53%, DRAM 45% busy under ncu). Tiles of 32 tokens 177 us, of 128 172; CTAs of 2 or 8
+// warps 171 and 173. One reciprocal for two sigmoids saves a quarter of the special functions and
+// no time, and loses saturated gates.
 #pragma once
 
 #include "layer_common.cuh"
@@ -20,8 +28,9 @@ namespace drscan {
 
 constexpr int CONV_MAX_SPLITS = 4;
 constexpr int CONV_WARPS = 4;
-constexpr int CONV_ROWS = 4;   // rows in flight per thread while four more are summed
-constexpr int CONV_CTAS = 4;    // per SM, at 128 registers (unbounded: 158 registers, 3 CTAs, slower)
+constexpr int CONV_ROWS = 4;  // rows in flight per thread while four more are summed (8, with the
+                              // registers of 3 CTAs per SM: 173 us)
+constexpr int CONV_CTAS = 4;  // per SM, at 128 registers (5 spill)
 
 struct ConvSplit {
     void* out;
@@ -52,10 +61,27 @@ __device__ __forceinline__ int split_of(const ConvArgs& a, int col) {
     return si;
 }
 
-// Sum over `lanes` (a power of two) neighbouring lanes.
-__device__ __forceinline__ float group_sum(float v, int lanes) {
-    for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+// Sum over LANES neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int off = LANES >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
+}
+
+// Runs `f` with the lanes of a normalised split's heads as a constant, 0 without the norm. (With the
+// count at run time the sums of neighbouring rows' squares wait for one another: 178 us instead of
+// 170.)
+template <int VEC, typename F>
+__device__ __forceinline__ void with_lanes(const ConvSplit& sp, F&& f) {
+    if (!sp.normalise)
+        f(std::integral_constant<int, 0>());
+    else if (sp.dim == 32)
+        f(std::integral_constant<int, 32 / VEC>());
+    else if (sp.dim == 64)
+        f(std::integral_constant<int, 64 / VEC>());
+    else
+        f(std::integral_constant<int, 128 / VEC>());
 }
 
 // The taps of one thread's channels, by pairs of channels (the sums run two to an instruction).
@@ -83,10 +109,9 @@ struct ConvTaps {
 };
 
 // One row: window (oldest first) and the new row x -> the activated, normalised outputs.
-template <int VEC, int K, bool SILU>
+template <int VEC, int K, bool SILU, int LANES>
 __device__ __forceinline__ void conv_row(const ConvTaps<VEC, K>& f, float2 (&win)[K - 1][VEC / 2],
-                                         const float2* x, bool normalise, int lanes, float eps,
-                                         float2* y) {
+                                         const float2* x, float eps, float2* y) {
     float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < VEC / 2; ++v) {
@@ -94,7 +119,7 @@ __device__ __forceinline__ void conv_row(const ConvTaps<VEC, K>& f, float2 (&win
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) c = fma2(f.w[j][v], win[j][v], c);
         y[v] = SILU ? mul2(c, sigmoid2(c)) : c;
-        if (normalise) ss = fma2(y[v], y[v], ss);
+        if (LANES > 0) ss = fma2(y[v], y[v], ss);
     }
 #pragma unroll
     for (int j = 0; j < K - 2; ++j)
@@ -102,8 +127,8 @@ __device__ __forceinline__ void conv_row(const ConvTaps<VEC, K>& f, float2 (&win
         for (int v = 0; v < VEC / 2; ++v) win[j][v] = win[j + 1][v];
 #pragma unroll
     for (int v = 0; v < VEC / 2; ++v) win[K - 2][v] = x[v];
-    if (normalise) {
-        const float r = rsqrtf(group_sum(ss.x + ss.y, lanes) + eps);
+    if (LANES > 0) {
+        const float r = rsqrtf(group_sum<LANES>(ss.x + ss.y) + eps);
 #pragma unroll
         for (int v = 0; v < VEC / 2; ++v) y[v] = mul2(y[v], make_float2(r, r));
     }
@@ -161,7 +186,6 @@ __global__ void __launch_bounds__(32 * CONV_WARPS, CONV_CTAS) short_conv_kernel(
     T* dst = static_cast<T*>(sp.out) + b * sp.sb + head * sp.sh + within * VEC;
     const T* src = xrow + (long)t0 * a.xst;
     dst += (long)t0 * sp.st;
-    const bool normalise = sp.normalise;
     // a group's rows are loaded while the group before is summed; rows behind the last are not read
     uint4 raw[CONV_ROWS];
     auto fetch = [&](int n) {
@@ -172,22 +196,25 @@ __global__ void __launch_bounds__(32 * CONV_WARPS, CONV_CTAS) short_conv_kernel(
         }
     };
     fetch(t1 - t0);
-    for (int t = t0; t < t1; t += CONV_ROWS) {
-        const int n = t1 - t;  // rows left
-        uint4 now[CONV_ROWS];
+    with_lanes<VEC>(sp, [&](auto lanes_of_head) {
+        constexpr int LANES = decltype(lanes_of_head)::value;
+        for (int t = t0; t < t1; t += CONV_ROWS) {
+            const int n = t1 - t;  // rows left
+            uint4 now[CONV_ROWS];
 #pragma unroll
-        for (int i = 0; i < CONV_ROWS; ++i) now[i] = raw[i];
-        if (n > CONV_ROWS) fetch(n - CONV_ROWS);
+            for (int i = 0; i < CONV_ROWS; ++i) now[i] = raw[i];
+            if (n > CONV_ROWS) fetch(n - CONV_ROWS);
 #pragma unroll
-        for (int i = 0; i < CONV_ROWS; ++i) {
-            float2 x[VEC / 2], y[VEC / 2];
-            Vec16<T>::unpack(now[i], reinterpret_cast<float*>(x));
-            conv_row<VEC, K, SILU>(f, win, x, normalise, lanes, a.eps, y);
-            if (live && i < n)
-                *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(reinterpret_cast<float*>(y));
-            dst += sp.st;
+            for (int i = 0; i < CONV_ROWS; ++i) {
+                float2 x[VEC / 2], y[VEC / 2];
+                Vec16<T>::unpack(now[i], reinterpret_cast<float*>(x));
+                conv_row<VEC, K, SILU, LANES>(f, win, x, a.eps, y);
+                if (live && i < n)
+                    *reinterpret_cast<uint4*>(dst) = Vec16<T>::pack(reinterpret_cast<float*>(y));
+                dst += sp.st;
+            }
         }
-    }
+    });
 }
 
 // One token per sequence on a resident state (the last K - 1 inputs, shifted in place). A warp
@@ -218,7 +245,9 @@ __global__ void __launch_bounds__(32 * CONV_WARPS) short_conv_step_kernel(
     for (int j = 0; j < K - 1; ++j) Vec16<T>::unpack(old[j], reinterpret_cast<float*>(win[j]));
     Vec16<T>::unpack(now, reinterpret_cast<float*>(x));
     const int lanes = sp.dim / VEC;
-    conv_row<VEC, K, SILU>(f, win, x, sp.normalise, lanes, a.eps, y);
+    with_lanes<VEC>(sp, [&](auto lanes_of_head) {
+        conv_row<VEC, K, SILU, decltype(lanes_of_head)::value>(f, win, x, a.eps, y);
+    });
     __syncwarp();  // idle lanes have read the last vector's state before its owner shifts it
     if (live) {
 #pragma unroll

@@ -29,6 +29,16 @@
 // Tiles are double-buffered, those of x apart from C and B, which are free as soon as the
 // products have read them; scores run ahead, so the only serial dependence between chunks is
 // state -> registers -> S copy -> inter. Every wait is bounded.
+//
+// Measured: 16 heads of P = N = 128, 8 x 4096 tokens (295 MB): 190 us; one
+// sequence of 32768 tokens, P = 64: 147 us in 9 segments. A chunk of 64 channels takes about 4,500
+// cycles, where its products take 1,500 on the tensor core and its shared memory traffic 2,700:
+// bound by the latency of the roles' instructions. They share the issue slots (51% busy) of four
+// schedulers, rows r of P always those of the scheduler that owns their lanes of tensor memory; the
+// weights of rows 96-127, with 4 of the 10 blocks, take 2,900 cycles a chunk. What was slower: weights
+// of the diagonal blocks made before the scores come, on 8 warps (235 us) or on 12 with 4 left to
+// scale x (242 us); the two warps of 32 rows at 64 columns each (193 us). 256 CTAs run in two waves on
+// 148 SMs, 86% full.
 #pragma once
 
 #include <algorithm>
@@ -524,8 +534,9 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
       }
     } else if (warp < 8) {
         // ------------------------------------------------------------------ P from the scores
-        // (two warps per 32 rows: the one weighs columns 0-63, the other 64-127. The P of 16 columns
-        // goes over the first half of their scores, so no warp writes what another reads.)
+        // (two warps per 32 rows, which take turns at 16 columns, so that both have their part of the
+        // diagonal block. The P of 16 columns goes over the first half of their scores, so no warp
+        // writes what another reads.)
         regs_down<SC_REG_P>();
         if constexpr (OUT) {
             const int i = tid & 127, rw = warp & 3;
@@ -538,9 +549,8 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 tc_fence_after();
                 const uint32_t tsc = trow + TC_SCORE + 128 * s;
                 // 16 columns at a time, in a loop, whose code stays in the instruction cache
-                const int left = 64 * (warp >> 2);
 #pragma unroll 1
-                for (int j0 = left; j0 < left + 64; j0 += 16) {
+                for (int j0 = 16 * (warp >> 2); j0 < SCK; j0 += 32) {
                     const int J = j0 >> 5;
                     uint32_t pk[8];
                     if (J <= rw) {
