@@ -30,9 +30,8 @@
 // products have read them; scores run ahead, so the only serial dependence between chunks is
 // state -> registers -> S copy -> inter. Every wait is bounded.
 //
-// Measured: 16 heads of P = N = 128, 8 x 4096 tokens (295 MB): 190 us; one
-// sequence of 32768 tokens, P = 64: 147 us in 9 segments. A chunk of 64 channels takes about 4,500
-// cycles, where its products take 1,500 on the tensor core and its shared memory traffic 2,700:
+// Measured: 16 heads of P = N = 128, 8 x 4096 tokens (295 MB): 190 us; one sequence of 32768
+// tokens, P = 64: 147 us in 9 segments. A chunk of 64 channels takes about 4,500 cycles, where its products take 1,500 on the tensor core and its shared memory traffic 2,700:
 // bound by the latency of the roles' instructions. They share the issue slots (51% busy) of four
 // schedulers, rows r of P always those of the scheduler that owns their lanes of tensor memory; the
 // weights of rows 96-127, with 4 of the 10 blocks, take 2,900 cycles a chunk. What was slower: weights
