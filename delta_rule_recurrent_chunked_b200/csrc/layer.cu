@@ -162,14 +162,18 @@ int dispatch_ssm_sequential(const SsmArgs& a, cudaStream_t stream) {
     return DR_ERR_UNSUPPORTED;
 }
 
-// Segments of the per-token scan: as many as leave each 64 tokens, up to four CTAs (of 32 rows) to
-// an SM. Both passes over a segment's tokens have to be well below one over all of them, with 6 us
-// for two launches more: from three segments on.
+// Segments of the per-token scan: of 32 tokens each, as far as four CTAs (of 32 rows) to an SM go,
+// from three segments on, where one pass over all tokens takes 20 us or more: 192 tokens at N = 32, 96
+// at N = 128. Two launches more and the scratch take the host 6 us. Measured on the device, fp32,
+// whole and in segments: N = 32, 2 x 4 heads: 200 tokens 23 and 12 us, 301 tokens 34 and 12; N = 128,
+// 4 heads: 100 tokens 25 and 16 us, 301 tokens 73 and 17; 32 heads of 128 x 128, 200 tokens 50 and
+// 45. (301 tokens in segments of 48: 14 and 22 us; of 80: 18 and 31.)
 void plan_ssm_sequential(SsmArgs* a) {
     a->nseg = 1;
     a->seg_len = a->T;
     const long ctas = (long)a->B * a->H * (a->P / SSM_ROWS);
-    const long most = std::min<long>(a->T / 64, 592 / ctas);
+    if ((long)a->T * (64 + a->N) < 192 * 96) return;
+    const long most = std::min<long>(((long)a->T + 31) / 32, 592 / ctas);
     if (most > 2) {
         a->seg_len = (int)(((a->T + most - 1) / most + SSM_TILE - 1) / SSM_TILE * SSM_TILE);
         a->nseg = (a->T + a->seg_len - 1) / a->seg_len;
