@@ -76,6 +76,7 @@ SIGNATURES = {
     "dr_status_string": ([_I], ctypes.c_char_p),
     "dr_poll_error": ([_VP], _I),
     "dr_debug_timeout_probe": ([_I, _VP], _I),
+    "dr_debug_wait_limit": ([_LL], _I),
     "dr_chunked_plan": ([_I, ctypes.c_longlong, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),
     "dr_chunked_plan_ex": ([_I, ctypes.c_longlong, _I, _I, _I, ctypes.POINTER(_I),
                             ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),

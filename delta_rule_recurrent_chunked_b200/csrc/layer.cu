@@ -212,6 +212,10 @@ int sm_count() {
     return n;
 }
 
+// Limit of a wait inside the chunked scan's launches of this host thread, in nanoseconds, or -1 for
+// the usual one (dr_debug_wait_limit).
+thread_local long long g_wait_ns = -1;
+
 SsmView as_view(const dr_view* v) {
     return v ? SsmView{v->data, (long)v->sb, (long)v->sh, (long)v->st} : SsmView{};
 }
@@ -386,11 +390,18 @@ int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_v
         a.seg_state = static_cast<float*>(scratch);
         a.seg_log = a.seg_state + states * PN;
     }
-    rc = chunked               ? launch_ssm_chunked(a, stream)
-         : (mode & DR_IN_BF16) ? dispatch_ssm_sequential<__nv_bfloat16>(a, stream)
-                               : dispatch_ssm_sequential<float>(a, stream);
+    rc = chunked && g_wait_ns < 0 ? launch_ssm_chunked<false>(a, 0, stream)
+         : chunked                ? launch_ssm_chunked<true>(a, (uint32_t)g_wait_ns, stream)
+         : (mode & DR_IN_BF16)    ? dispatch_ssm_sequential<__nv_bfloat16>(a, stream)
+                                  : dispatch_ssm_sequential<float>(a, stream);
     if (scratch && cudaFreeAsync(scratch, stream) != cudaSuccess && rc == DR_OK) rc = DR_ERR_CUDA;
     return rc;
+}
+
+int dr_debug_wait_limit(long long limit_ns) {
+    if (limit_ns < -1 || limit_ns > (long long)DRSCAN_WAIT_LIMIT_NS) return DR_ERR_INVALID_ARG;
+    g_wait_ns = limit_ns;
+    return DR_OK;
 }
 
 int ssm_step(const dr_view* x, const dr_view* dt, const float* A, const dr_view* Bm,

@@ -28,7 +28,8 @@
 // scores and the outputs, warps 28-31 prepare the per-token factors, up to four chunks ahead.
 // Tiles are double-buffered, those of x apart from C and B, which are free as soon as the
 // products have read them; scores run ahead, so the only serial dependence between chunks is
-// state -> registers -> S copy -> inter. Every wait is bounded.
+// state -> registers -> S copy -> inter. Every wait is bounded; a role whose wait runs out leaves
+// its loop, and the loads and products that it started are waited for before the CTA ends.
 //
 // Measured: 16 heads of P = N = 128, 8 x 4096 tokens (295 MB): 190 us; one sequence of 32768
 // tokens, P = 64: 147 us in 9 segments. A chunk of 64 channels takes about 4,500 cycles, where its products take 1,500 on the tensor core and its shared memory traffic 2,700:
@@ -101,7 +102,7 @@ enum {
     SB_YFREE = 27,   // inter and intra products have been read
     SB_XS = 28,      // [SC_NXS] scaled x of 32 tokens is in its slot
     SB_XSFREE = 31,  // [4] .. of the chunk's quarter has been read
-    SB_DRAIN = 35,   // [3] after a timeout
+    SB_DRAIN = 35,   // [3] all that an MMA warp issued is over
     SB_COUNT = 38
 };
 constexpr int SC_TOTAL = SC_BAR + 8 * SB_COUNT + 32;
@@ -173,18 +174,53 @@ __device__ __forceinline__ void commit_elected(uint32_t bar) {
         : "memory");
 }
 
+// The lower 32 bits of the timer in nanoseconds (they come round after 4.3 s).
+__device__ __forceinline__ uint32_t timer_lo_ns() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+// Whether the phase with the given parity is over. (mbar_test may suspend the thread for some
+// microseconds until it is.)
+__device__ __forceinline__ bool mbar_test_now(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits, as a whole warp, for the phase with the given parity: by a vote, since lanes that leave
-// the polls at different times would run what follows one after another. The wait is bounded by
-// its polls (a poll takes some 20 cycles to some microseconds, so 2^20 of them at least 10 ms,
-// a thousand times the longest wait for memory, and seconds at most). False (with the status
-// latched) when they ran out: the caller leaves its loop, and whoever waits for it runs out too.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
-    int polls = 1 << 20;
+// the polls at different times would run what follows one after another. Bounded by its polls: one
+// that fails suspends the warp for 4 us (3.96 measured, from 10 to 300000 polls in a row), so that
+// they last for DRSCAN_WAIT_LIMIT_NS. False (with the status latched) when they ran out: the caller
+// leaves its loop, and whoever waits for it runs out too. (With a look at the clock in the loop, in
+// whatever form, the scan of 8 x 16 heads and 4096 tokens took 183 to 223 us instead of 173.)
+// TIMED, for tests: no suspension, and `limit` nanoseconds (0: one poll) instead.
+template <bool TIMED>
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t limit) {
+    if constexpr (TIMED) {
+        const uint32_t t0 = timer_lo_ns();
 #pragma unroll 1
-    while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
-        if (--polls == 0) {
-            raise_status(DR_ERR_TIMEOUT);
-            return false;
+        while (!__all_sync(0xffffffffu, mbar_test_now(bar, parity))) {
+            if (__any_sync(0xffffffffu, timer_lo_ns() - t0 >= limit)) {
+                raise_status(DR_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    } else {
+        int polls = (int)(DRSCAN_WAIT_LIMIT_NS / 4000);
+#pragma unroll 1
+        while (!__all_sync(0xffffffffu, mbar_test(bar, parity))) {
+            if (--polls == 0) {
+                raise_status(DR_ERR_TIMEOUT);
+                return false;
+            }
         }
     }
     return true;
@@ -235,22 +271,17 @@ __device__ __forceinline__ void tma_prefetch_4d(const void* map, int c0, int c1,
                  : "memory");
 }
 
-// After an abort: waits (bounded) for the async work of a phase that was started.
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_test(bar, parity) && global_timer_ns() - t0 < DRSCAN_WAIT_LIMIT_NS) {
-    }
-}
-
 struct SsmChunkArgs {
     SsmArgs s;
     // 1 where the tensor map's head / batch coordinate counts, 0 where the view repeats
     int xh, xb, bh, bb, ch, cb;
     int out32;  // the rows of out lie on 32-byte boundaries
+    uint32_t wait_ns;  // limit of a wait of one role for another (TIMED)
 };
 
-// grid: (B * H * slices of SCV value channels, segments of this pass); block: SC_THREADS.
-template <int PASS>
+// grid: (B * H * slices of SCV value channels, segments of this pass); block: SC_THREADS. TIMED:
+// waits with a limit of the caller's, for tests of what happens when they run out.
+template <int PASS, bool TIMED>
 __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
     const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmB,
     const __grid_constant__ CUtensorMap tmC, const __grid_constant__ SsmChunkArgs ca) {
@@ -269,14 +300,17 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
     };
     // waits of chunk c
     auto wait2 = [&](int i, int c) {
-        return mbar_wait_warp(bar(i + (c & 1)), (uint32_t)((c >> 1) & 1));
+        return mbar_wait_warp<TIMED>(bar(i + (c & 1)), (uint32_t)((c >> 1) & 1), ca.wait_ns);
     };
     auto wait1 = [&](int i, int c) {
-        return mbar_wait_warp(bar(i), (uint32_t)(c & 1));
+        return mbar_wait_warp<TIMED>(bar(i), (uint32_t)(c & 1), ca.wait_ns);
     };
     auto wait_par = [&](int c) {
-        return mbar_wait_warp(bar(SB_PAR + c % SC_NPAR), (uint32_t)((c / SC_NPAR) & 1));
+        return mbar_wait_warp<TIMED>(bar(SB_PAR + c % SC_NPAR), (uint32_t)((c / SC_NPAR) & 1),
+                              ca.wait_ns);
     };
+    // waits for async work that was started, whatever limit the others have
+    auto drain = [&](int i, uint32_t parity) { mbar_wait_warp<false>(bar(i), parity, 0); };
 
     // (by a shuffle, so that the compiler knows the roles' branches to be uniform: without it the
     // two issuing warps' code is more than twice as long)
@@ -347,8 +381,8 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
         static_assert(SC_NPAR == 4, "a slot of factors per warp");
         int c = warp - 28;
         for (; c < nc; c += SC_NPAR) {
-            if (c >= SC_NPAR && !mbar_wait_warp(bar(SB_PARFREE + c % SC_NPAR),
-                                                (uint32_t)((c / SC_NPAR - 1) & 1)))
+            if (c >= SC_NPAR && !mbar_wait_warp<TIMED>(bar(SB_PARFREE + c % SC_NPAR),
+                                                (uint32_t)((c / SC_NPAR - 1) & 1), ca.wait_ns))
                 break;
             SsmChunkPar* pr = par(c % SC_NPAR);
 #pragma unroll 1
@@ -442,15 +476,19 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             }
             __syncwarp();
         }
-        // a wait ran out: loads in flight may not outlive the CTA
-        if (c < nc) {
+        // Nothing asynchronous may outlive the CTA: neither the commits that free the last tiles
+        // (nobody else waits for them) nor, where a wait of any role ran out, the last loads
+        if (c == nc) {
 #pragma unroll 1
-            for (int k = max(0, loaded_cb - 2); k < loaded_cb; ++k)
-                mbar_drain(bar(SB_CB + (k & 1)), (uint32_t)((k >> 1) & 1));
-#pragma unroll 1
-            for (int k = max(0, c - 2); k < c; ++k)
-                mbar_drain(bar(SB_X + (k & 1)), (uint32_t)((k >> 1) & 1));
+            for (int k = max(0, nc - 2); k < nc; ++k)
+                if (!wait2(SB_CBFREE, k) || !wait2(SB_XFREE, k)) break;
         }
+#pragma unroll 1
+        for (int k = max(0, loaded_cb - 2); k < loaded_cb; ++k)
+            drain(SB_CB + (k & 1), (uint32_t)((k >> 1) & 1));
+#pragma unroll 1
+        for (int k = max(0, c - 2); k < c; ++k)
+            drain(SB_X + (k & 1), (uint32_t)((k >> 1) & 1));
       } else {
         // ------------------------------------------------------------------ MMAs
         // (whole warps, converged: see mma_ss. Three of them, so that no product waits for what
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 bool ok = true;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {  // 32 tokens at a time
-                    if (!(ok = mbar_wait_warp(bar(SB_XS + slot), turn))) break;
+                    if (!(ok = mbar_wait_warp<TIMED>(bar(SB_XS + slot), turn, ca.wait_ns))) break;
                     uint64_t db =
                         smem_desc_sw128(base + SC_XS + slot * 3 * SC_XPART, SC_XPART, 1024);
 #pragma unroll 1
@@ -525,10 +563,11 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                 commit_elected(bar(SB_XFREE + s));
             }
         }
-        if (c < n) {  // a wait ran out: products in flight may not outlive the CTA's memory
-            const uint32_t b0 = bar(SB_DRAIN + warp - 25);
-            commit_elected(b0);
-            mbar_drain(b0, 0);
+        // products and commits in flight may not outlive the CTA's memory: those of a role whose
+        // wait ran out, or whose results nobody took up since another's did
+        if (n > 0 && (OUT || warp == 25)) {
+            commit_elected(bar(SB_DRAIN + warp - 25));
+            drain(SB_DRAIN + warp - 25, 0);
         }
       }
     } else if (warp < 8) {
@@ -655,7 +694,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             // waited for it, so parity tells its phases apart.)
             const uint32_t use = 4 * c + q, slot = use % SC_NXS, last = use - SC_NXS;
             if (use >= SC_NXS &&
-                !mbar_wait_warp(bar(SB_XSFREE + (last & 3)), (last >> 2) & 1))
+                !mbar_wait_warp<TIMED>(bar(SB_XSFREE + (last & 3)), (last >> 2) & 1, ca.wait_ns))
                 break;
             uint8_t* to = sm + SC_XS + slot * 3 * SC_XPART + lane * 128;
 #pragma unroll
@@ -885,11 +924,11 @@ inline void plan_ssm_chunked(SsmArgs* a, int sms) {
     a->nseg = (nc + len - 1) / len;
 }
 
-template <int PASS>
+template <int PASS, bool TIMED>
 int launch_ssm_chunked_pass(const CUtensorMap& mx, const CUtensorMap& mb, const CUtensorMap& mc,
                             const SsmChunkArgs& ca, long gx, int gy, cudaStream_t stream) {
     const int smem = SC_TOTAL + 1024;
-    auto kern = ssm_chunked_kernel<PASS>;
+    auto kern = ssm_chunked_kernel<PASS, TIMED>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
         cudaSuccess)
         return DR_ERR_CUDA;
@@ -898,9 +937,11 @@ int launch_ssm_chunked_pass(const CUtensorMap& mx, const CUtensorMap& mb, const 
 }
 
 // The planned passes (a.nseg, a.seg_len and the scratch set).
-inline int launch_ssm_chunked(const SsmArgs& a, cudaStream_t stream) {
+template <bool TIMED>
+int launch_ssm_chunked(const SsmArgs& a, uint32_t wait_ns, cudaStream_t stream) {
     SsmChunkArgs ca;
     ca.s = a;
+    ca.wait_ns = wait_ns;
     CUtensorMap mx, mb, mc;
     if (!ssm_map(&mx, a.x, a.P, a.T, a.H, a.B, &ca.xh, &ca.xb) ||
         !ssm_map(&mb, a.Bm, a.N, a.T, a.G, a.B, &ca.bh, &ca.bb) ||
@@ -911,11 +952,12 @@ inline int launch_ssm_chunked(const SsmArgs& a, cudaStream_t stream) {
     const long gx = (long)a.B * a.H * ((a.P + SCV - 1) / SCV);
     if (gx > 0x7fffffffl || a.nseg > 65535) return DR_ERR_UNSUPPORTED;
     if (a.nseg > 1) {
-        int rc = launch_ssm_chunked_pass<SSM_PASS_STATES>(mx, mb, mc, ca, gx, a.nseg - 1, stream);
+        int rc = launch_ssm_chunked_pass<SSM_PASS_STATES, TIMED>(mx, mb, mc, ca, gx,
+                                                                 a.nseg - 1, stream);
         if (rc == DR_OK) rc = launch_ssm_chain(a, stream);
         if (rc != DR_OK) return rc;
     }
-    return launch_ssm_chunked_pass<SSM_PASS_OUTPUTS>(mx, mb, mc, ca, gx, a.nseg, stream);
+    return launch_ssm_chunked_pass<SSM_PASS_OUTPUTS, TIMED>(mx, mb, mc, ca, gx, a.nseg, stream);
 }
 
 }  // namespace drscan

@@ -534,6 +534,15 @@ int dr_segment_counters(unsigned long long* scans, unsigned long long* reruns);
  */
 int dr_debug_timeout_probe(int spin_limit, cudaStream_t stream);
 
+/*
+ * Test hook for the failure path of the chunked kernel of ssm_scan_fwd: the calls of this host
+ * thread that follow give up on a wait inside the kernel after `limit_ns` nanoseconds (0: after one
+ * poll; at most 2000000000, about the usual limit, which -1 restores). A call that gave up latches
+ * DR_ERR_TIMEOUT, waits for the copies and products that it has in flight and returns; its
+ * outputs hold nothing of use. Returns DR_OK or DR_ERR_INVALID_ARG; launches nothing.
+ */
+int dr_debug_wait_limit(long long limit_ns);
+
 /* Library version as 10000*major + 100*minor + patch. */
 int dr_version(void);
 
