@@ -73,11 +73,12 @@ constexpr int SC_XS = 2 * SC_STAGE;
 constexpr int SC_S = SC_XS + SC_NXS * 3 * SC_XPART;      // S^T rows n, 64 value channels
 constexpr int SC_PAR = SC_S + SC_PANEL;                  // [SC_NPAR] SsmChunkPar
 struct SsmChunkPar {
-    float g2[SCK];     // g_i log2(e)
+    float g2[SCK];     // (g_i - g before the token's block of 32) log2(e)
     float delta[SCK];
     float u[SCK];      // delta_j exp(g_end(J) - g_j), J the token's block of 32
     float w[SCK];      // delta_j exp(g_Q - g_j)
     float eg[SCK];     // exp(g_i)
+    float between[16]; // [4 I + J] log2(e) times the steps of the blocks between J and I, J < I
     float gamma;       // exp(g_Q)
     float pad[3];
 };
@@ -391,12 +392,15 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                                    ? ssm_delta(a, h, ssm_dt(a, b, h, (long)t0 + c * SCK + t))
                                    : 0.f;
             __syncwarp();
-            // four neighbouring tokens per lane: sums from the chunk's left (inclusive) and right
-            // (exclusive: short near the chunk's end, where the weights of the state are largest)
+            // four neighbouring tokens per lane, eight lanes a block of 32: sums from the block's
+            // left (inclusive) and right (exclusive); those of whole blocks lead on to the chunk's
+            // ends. Only weights inside a block are then differences of sums.
             const float4 d = *reinterpret_cast<const float4*>(&pr->delta[4 * lane]);
-            // a decay below 2^-160 is none at all in fp32; taken as 2^-160 it keeps g within 128 * 160,
-            // where differences of g are exact to 2^-9 (a token that wipes the state may decay by far
-            // more, and would drown the steps behind it)
+            // A decay below 2^-160 is none at all in fp32. Taken as 2^-160 it keeps the sums of a
+            // block within 32 * 160, where an addition is off by 2^-12 at most and a difference of
+            // two sums (some three additions of that size each) by 2^-9.4, 0.1 % of a weight: a
+            // token that wipes the state may decay by far more, and would drown the steps behind
+            // it.
             const auto step = [Ah](float dt) {
                 const float l = dt * Ah;
                 return l < -160.f ? -160.f : l;
@@ -404,29 +408,38 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
             const float l0 = step(d.x), l1 = step(d.y), l2 = step(d.z), l3 = step(d.w);
             const float q1 = l0 + l1, q2 = q1 + l2, q3 = q2 + l3;
             float left = q3, right = q3;
+            const int at = lane & 7, block = lane >> 3;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float x = __shfl_up_sync(0xffffffffu, left, off);
-                const float y = __shfl_down_sync(0xffffffffu, right, off);
-                if (lane >= off) left += x;
-                if (lane + off < 32) right += y;
+            for (int off = 1; off < 8; off <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, left, off, 8);
+                const float y = __shfl_down_sync(0xffffffffu, right, off, 8);
+                if (at >= off) left += x;
+                if (at + off < 8) right += y;
             }
-            const float total = __shfl_sync(0xffffffffu, left, 31);
-            float lx = __shfl_up_sync(0xffffffffu, left, 1);
-            float rx = __shfl_down_sync(0xffffffffu, right, 1);
-            if (lane == 0) lx = 0.f;
-            if (lane == 31) rx = 0.f;
+            float lx = __shfl_up_sync(0xffffffffu, left, 1, 8);
+            float rx = __shfl_down_sync(0xffffffffu, right, 1, 8);
+            if (at == 0) lx = 0.f;
+            if (at == 7) rx = 0.f;
+            const float b0 = __shfl_sync(0xffffffffu, left, 7), b1 = __shfl_sync(0xffffffffu, left, 15),
+                        b2 = __shfl_sync(0xffffffffu, left, 23), b3 = __shfl_sync(0xffffffffu, left, 31);
+            const float before = block == 0 ? 0.f : block == 1 ? b0 : block == 2 ? b0 + b1 : b0 + b1 + b2;
+            const float after = block == 3 ? 0.f : block == 2 ? b3 : block == 1 ? b2 + b3 : b1 + b2 + b3;
+            const float total = (b0 + b1) + (b2 + b3);
             const float4 gp = make_float4(lx + l0, lx + q1, lx + q2, lx + q3);
-            const float end = __shfl_sync(0xffffffffu, gp.w, lane | 7);  // of the block of 32
+            const float4 rp = make_float4(rx + l1 + l2 + l3, rx + l2 + l3, rx + l3, rx);
             *reinterpret_cast<float4*>(&pr->g2[4 * lane]) = gp;
             *reinterpret_cast<float4*>(&pr->u[4 * lane]) =
-                make_float4(d.x * ex2(end - gp.x), d.y * ex2(end - gp.y), d.z * ex2(end - gp.z),
-                            d.w * ex2(end - gp.w));
+                make_float4(d.x * ex2(rp.x), d.y * ex2(rp.y), d.z * ex2(rp.z), d.w * ex2(rp.w));
             *reinterpret_cast<float4*>(&pr->w[4 * lane]) =
-                make_float4(d.x * ex2(rx + l1 + l2 + l3), d.y * ex2(rx + l2 + l3),
-                            d.z * ex2(rx + l3), d.w * ex2(rx));
+                make_float4(d.x * ex2(rp.x + after), d.y * ex2(rp.y + after),
+                            d.z * ex2(rp.z + after), d.w * ex2(rp.w + after));
             *reinterpret_cast<float4*>(&pr->eg[4 * lane]) =
-                make_float4(ex2(gp.x), ex2(gp.y), ex2(gp.z), ex2(gp.w));
+                make_float4(ex2(gp.x + before), ex2(gp.y + before), ex2(gp.z + before),
+                            ex2(gp.w + before));
+            if (lane < 16) {
+                const int apart = (lane >> 2) - (lane & 3);
+                pr->between[lane] = apart == 3 ? b1 + b2 : apart == 2 ? (lane & 3 ? b2 : b1) : 0.f;
+            }
             if (lane == 0) pr->gamma = decay_f32(total * 0.6931471805599453f);
             logsum += total;
             __syncwarp();
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(SC_THREADS, 1) ssm_chunked_kernel(
                         float2 x[8];
                         tmem_ld16(tsc + j0, reinterpret_cast<float*>(x));
                         if (J < rw) {
-                            const float r = ex2(gi - pr->g2[32 * J + 31]);
+                            const float r = ex2(gi + pr->between[4 * rw + J]);
                             const float4* u = reinterpret_cast<const float4*>(pr->u + j0);
                             tmem_wait_ld();
 #pragma unroll
