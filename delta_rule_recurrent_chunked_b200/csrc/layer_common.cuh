@@ -82,7 +82,11 @@ __device__ __forceinline__ float rcp(float x) {
     return r;
 }
 
-// 1 / (1 + e^-x), of two values. e^-x overflows to infinity for x < -88, where the quotient is 0.
+// 1 / (1 + e^-x), of two values. e^-x overflows to infinity for x < -88, where the quotient is 0. The
+// rounding of x log2(e) moves the result by up to 1.3 |x| half steps of fp32 for x < 0, more than the
+// approximate functions do. That is far below a step of bf16, and for fp32 a choice: by way of expf
+// and a division the gated norm of 8 x 4096 tokens of 16 heads of 128 takes 164 us instead of 123, the
+// convolution of 8 x 2048 tokens of 6144 channels 163 instead of 155.
 __device__ __forceinline__ float2 sigmoid2(float2 x) {
     const float2 z = mul2(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
     const float2 d = add2(make_float2(ex2(z.x), ex2(z.y)), make_float2(1.f, 1.f));

@@ -2,7 +2,9 @@
  * drscan: forward recurrent-memory scan of delta-rule linear attention on B200 (sm_100a).
  *
  * C ABI. Every tensor argument is a DEVICE pointer owned by the caller, row-major and
- * contiguous (or a dr_view, which carries strides); the library never allocates, frees or keeps a pointer past the call.
+ * contiguous (or a dr_view, which carries strides); the library never frees one or keeps it past
+ * the call. The only memory that it takes itself is scratch from a stream-ordered pool of its own,
+ * given back on the same stream before the call returns, where a function's description says so.
  * Calls are asynchronous on `stream`: the return value covers argument validation and
  * the kernel launch only. Conditions detected on the device (a bounded wait that ran
  * out) are latched in a per-device status word and read by dr_poll_error().
@@ -373,14 +375,16 @@ typedef struct conv_split {
  *                for zeros
  *   lengths      [B] int32 on the device, or NULL: tokens of each sequence (clamped to 0..T).
  *                Outputs of later rows are left as they were; rows of x behind a sequence are
- *                read but reach nothing
+ *                not read
  *   splits       nsplit <= 4 host structs; sum of heads * dim = C; out like x
  *   state_final  [B,K-1,C] like x: the last K - 1 inputs of each sequence (of state0 and x
  *                together where it is shorter), or NULL to skip; not state0 itself
  *   mode         DR_IN_BF16? | CONV_SILU?
  *
  * Supported: K in {2,3,4}, dim in {32, 64, 128}, T <= 16776960; T = 0 copies state0. Sums in
- * fp32, one rounding per output. Outputs may not alias inputs. Returns DR_OK or a negative status; on error nothing is launched.
+ * fp32, one rounding per output. sigmoid(c) is right to (1.3 |c| + 8) 2^-24 of itself (the argument
+ * of its exponential is an fp32 value) and 0 below 2^-126. Outputs may not alias inputs. Returns
+ * DR_OK or a negative status; on error nothing is launched.
  */
 int short_conv_fwd(const dr_view* x, const float* weight, const float* bias, const void* state0,
                    const int* lengths, const conv_split* splits, int nsplit, void* state_final,
@@ -410,19 +414,20 @@ int short_conv_step(const dr_view* x, const float* weight, const float* bias, vo
  *   S0       [B,H,P,N] fp32 or NULL for zeros; S_final the same or NULL to skip; not S0 itself
  *   lengths  [B] int32 on the device or NULL: tokens of each sequence (clamped to 0..T). Rows
  *            of out behind a sequence are left as they were, whatever x, dt, Bm and Cm hold
- *            there; S_final is the state after the last token
+ *            there (rows of x, Bm and Cm may be read); S_final is the state after the last token
  *   mode     DR_IN_BF16? | SSM_DT_SOFTPLUS? | SSM_DT_BF16? | DR_FORCE_SEQUENTIAL?
  *
  * Supported: P, N in {32, 64, 128}, H a multiple of G, T <= 2^30. bf16 inputs of more than
  * 2048 / N tokens run the chunked kernel (128-token chunks on tcgen05 tensor cores; weights of a
  * chunk's tokens and the state that the outputs read in bf16, the state itself in fp32
- * throughout), everything else the per-token kernel on CUDA cores. The steps decay: delta A <= 0 (growth is computed as written
- * while exp stays finite). A NaN or infinity among a sequence's own x, Bm, Cm or dt reaches outputs
+ * throughout), everything else the per-token kernel on CUDA cores. The steps decay:
+ * delta A <= 0 (growth is computed as written while exp stays finite). A NaN or infinity among a sequence's own x, Bm, Cm or dt reaches outputs
  * of its whole 128-token chunk in the chunked kernel. Sequences too few to fill the GPU are cut into
  * segments, whose states take B*H*(segments-1)*(P*N+1) floats of scratch from the library's
  * stream-ordered pool (DR_ERR_CUDA if it cannot be had); the result is that of the uncut scan
  * up to fp32 rounding. T = 0 copies S0. out may not alias an input. Returns DR_OK or a negative
- * status; on error nothing is launched.
+ * status: DR_ERR_INVALID_ARG and DR_ERR_UNSUPPORTED with nothing launched; after DR_ERR_CUDA some of
+ * a segmented scan's launches may have been made, and out and S_final hold nothing of use.
  */
 int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_view* Bm,
                  const dr_view* Cm, const float* D, const float* dt_bias, const float* S0,
@@ -453,7 +458,7 @@ int ssm_step(const dr_view* x, const dr_view* dt, const float* A, const dr_view*
  *   mode    DR_IN_BF16? | NORM_SIGMOID? | NORM_GATE_FIRST? | NORM_SHARED_WEIGHT?
  *
  * Supported: d in {32, 64, 128}, W <= 16384 (bf16) or 8192 (fp32), B*T*(H/norm_heads) < 2^31.
- * Statistics in fp32, one rounding per output. out may not alias y; it may be gate itself, with
+ * Statistics in fp32, one rounding per output; sigmoid(gate) as in short_conv_fwd. out may not alias y; it may be gate itself, with
  * the same strides.
  */
 int gated_norm_fwd(const dr_view* y, const dr_view* gate, const float* weight, const dr_view* out,
