@@ -372,10 +372,12 @@ int ssm_scan_fwd(const dr_view* x, const dr_view* dt, const float* A, const dr_v
     a.S0 = S0;
     a.S_final = S_final;
     a.lengths = lengths;
-    // The chunked kernel takes about 8 us for up to 128 tokens of any N (16 heads, P 64), the
-    // per-token kernel some 2 us and 0.25 us a token at N = 128, 0.1 us at N = 32 (7.8 against 6.7
-    // us at 16 tokens and N = 128, 7.4 against 9.4 at 64 tokens and N = 32; at 2048 heads 102
-    // against 97 and 95 against 50).
+    // By the tokens alone, fitted to few heads. Device time (P 64) of the chunked kernel and the
+    // per-token one: N = 128, 16 heads: 17 tokens 7.8 and 6.5 us, 33 tokens 8.0 and 9.9, 128 tokens
+    // 8.7 and 17.4; N = 32: 65 tokens 8.2 and 9.4, 128 tokens 8.6 and 15.4. With more heads the two
+    // meet later, and just above the limit the per-token kernel would be faster: 256 heads 15.6 and
+    // 11.4 (17 tokens, N = 128), 16.2 and 15.4 (65, N = 32), 2048 heads 97 and 65, 101 and 82; from
+    // twice the limit on the chunked kernel is (2048 heads: 100 and 113, 117 and 156).
     const bool chunked = (mode & DR_IN_BF16) && !(mode & DR_FORCE_SEQUENTIAL) &&
                          (long)T * N > 2048 && ssm_chunked_fits(a);
     if (chunked)

@@ -16,8 +16,8 @@
 // Measured, q, k and v of 16 heads of 128 (6144 bf16 channels, q and k normalised) for 8 x 4096
 // tokens, 805 MB: 170 us, 4.7 TB/s, 73% of the measured copy rate. The loads and stores alone take
 // 137 us, without SiLU 158: the rest is the issue and latency of some hundred instructions per
-// 16 bytes on the 16 warps that the window and the taps leave room for (issue slots 50%, special
-// functions 53%, DRAM 45% busy under ncu). Tiles of 32 tokens 177 us, of 128 172; CTAs of 2 or 8
+// 16 bytes on the 16 warps that the window and the taps leave room for (issue slots 45%, special
+// functions 56%, DRAM 48% busy under ncu). Tiles of 32 tokens 177 us, of 128 172; CTAs of 2 or 8
 // warps 171 and 173. Vectors of 8 bytes leave room for 20 to 28 warps and take 174 to 179, more
 // instructions and shuffles a byte. Fewer instructions saved no time: taps scaled for 2^x (172), one
 // reciprocal for two sigmoids (171, and it loses saturated gates); the loop unrolled twice took 181.

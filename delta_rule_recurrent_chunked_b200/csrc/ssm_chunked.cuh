@@ -27,15 +27,23 @@
 // write the outputs, warp 24 loads the tiles by TMA, warps 25-27 issue the MMAs of the state, the
 // scores and the outputs, warps 28-31 prepare the per-token factors, up to four chunks ahead.
 // Tiles are double-buffered, those of x apart from C and B, which are free as soon as the
-// products have read them; scores run ahead, so the only serial dependence between chunks is
-// state -> registers -> S copy -> inter. Every wait is bounded; a role whose wait runs out leaves
-// its loop, and the loads and products that it started are waited for before the CTA ends.
+// products have read them; scores run ahead. Every wait is bounded; a role whose wait runs out
+// leaves its loop, and the loads and products that it started are waited for before the CTA ends.
 //
-// Measured: 16 heads of P = N = 128, 8 x 4096 tokens (295 MB): 190 us; one sequence of 32768
-// tokens, P = 64: 147 us in 9 segments. A chunk of 64 channels takes about 4,500 cycles, where its products take 1,500 on the tensor core and its shared memory traffic 2,700:
-// bound by the latency of the roles' instructions. They share the issue slots (51% busy) of four
+// Three chains lead from chunk to chunk: state product -> registers -> S copy -> inter; the one set
+// of output accumulators, since inter(c) waits until the output warps have drained both products of
+// c - 1; and the S copy, which waits for the chunk's inter and intra products (SB_Y) though only
+// inter reads it.
+//
+// Measured: 16 heads of P = N = 128, 8 x 4096 tokens (295 MB): 196 us; one sequence of 32768
+// tokens, P = 64: 150 us in 9 segments. A chunk of 64 channels takes some 5,000 cycles, where its
+// products take 1,500 on the tensor core and its shared memory traffic 2,700: bound by those chains
+// and by the latency of the roles' instructions in them. With clocks in the waits (which slow a
+// chunk to 6,800) the drain takes 3,000 cycles of a chunk; the outputs' MMA warp waits 2,250 for the
+// S copy and 1,200 for the drain, 350 for the cleared tile of x and 180 for P; the state warps wait
+// 2,100 for their product and 700 for SB_Y. The roles share the issue slots (52% busy) of four
 // schedulers, rows r of P always those of the scheduler that owns their lanes of tensor memory; the
-// weights of rows 96-127, with 4 of the 10 blocks, take 2,900 cycles a chunk. What was slower: weights
+// weights of rows 96-127, with 4 of the 10 blocks, took 2,900 cycles a chunk. What was slower: weights
 // of the diagonal blocks made before the scores come, on 8 warps (235 us) or on 12 with 4 left to
 // scale x (242 us); the two warps of 32 rows at 64 columns each (193 us). 256 CTAs run in two waves on
 // 148 SMs, 86% full.
@@ -916,8 +924,9 @@ inline bool ssm_chunked_fits(const SsmArgs& a) {
 
 // Segments of a chunked scan: the count with the least time by a model in units of one chunk with
 // outputs (2.9 us): a chunk without takes SC_STATES, a CTA SC_START to begin and to end, the two
-// more launches SC_LAUNCHES and SC_CHAIN for each state that they chain. Measured for 16 heads of
-// 64 channels and 256 chunks: 9 segments (one wave of CTAs) 147 us, 37 (four waves) 186 us.
+// more launches SC_LAUNCHES and SC_CHAIN for each state that they chain. Fitted to 16 heads of 64
+// channels and 256 chunks, where 9 segments (one wave of CTAs) took 147 us and 37 (four waves) 186;
+// other shapes were not fitted.
 constexpr float SC_STATES = 0.55f, SC_START = 1.5f, SC_LAUNCHES = 2.f, SC_CHAIN = 0.05f;
 
 inline void plan_ssm_chunked(SsmArgs* a, int sms) {

@@ -14,7 +14,9 @@
 // reads and three shuffles for the readout. Bound: those reads (4 cycles each per warp and SM; with
 // one row per thread they took twice the time: 301 tokens of 128-element rows 79 us), or, with few
 // rows, the latency of the chain of tokens; the entry point then cuts the tokens into segments. (2 x
-// 4 ragged heads of 32 x 32 and 301 tokens, fp32: 12 us on the device in 10 segments.)
+// 4 ragged heads of 32 x 32 and 301 tokens, fp32: 12 us on the device in 10 segments.) Where the
+// kernel and not its launches sets the time, fp32, heads of 128 x 128: 16 heads, 4096 tokens 306 us
+// (floor 11), 8 x 16 heads 1817 us (90): 27 and 37 rows of S and tokens in a nanosecond.
 //
 // Segments (exact): the recurrence is affine in the state it enters with, S_out = (prod a) S_in
 // + S_zero. A first launch runs every segment but the last from zero (the first from S0)
@@ -310,7 +312,7 @@ inline int launch_ssm_chain(const SsmArgs& a, cudaStream_t stream) {
 // One token on a resident state: S is read and written once, which bounds the step (8 P N bytes
 // a head). A row of S is N / 4 lanes of 16 bytes, so a warp's access covers 128 / N rows in one
 // 512-byte piece; each warp owns SSM_STEP_U such pieces, all loaded before the first is used. 128
-// sequences of 32 heads of 128 x 128 (539 MB): 86 us, 97% of the measured copy rate.
+// sequences of 32 heads of 128 x 128 (539 MB): 87 us, 96% of the measured copy rate.
 constexpr int SSM_STEP_U = 4;
 constexpr int SSM_STEP_WARPS = 4;
 
